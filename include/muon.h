@@ -1,6 +1,7 @@
 /*
- * muon.h — C ABI of the MI355X (gfx950) Muon optimizer step (and the AdamW
- * step a hybrid Muon optimizer runs on its other parameters, declared below).
+ * muon.h — C ABI of the MI355X (gfx950) Muon optimizer step (and, declared
+ * below, the AdamW step a hybrid Muon optimizer runs on its other parameters
+ * and the layer operators that make the gradients both read).
  *
  * One Muon call performs one optimizer step on 2-D hidden-layer weight matrices:
  *
@@ -257,6 +258,116 @@ int muon_adamw_step(void* P, const void* G, float* m, float* v, int64_t n, int d
  * shared betas, eps and step.  `tensors` is a HOST array. */
 int muon_adamw_step_grouped(const muon_adamw_tensor* tensors, int64_t count, int dtype,
                             double beta1, double beta2, double eps, int64_t step, void* stream);
+
+/*
+ * Layer operators: what a training step computes around the hidden weights
+ * and hands to the steps above.  Layer norm gives y forward and dx, dgain and
+ * dbias backward (gain and bias are the hybrid optimizer's AdamW vectors);
+ * an activation checkpoint keeps a layer's input in 8 bits between the two
+ * passes; the weight gradient reads such a checkpoint and writes the G that
+ * muon_step reads.
+ *
+ * Checkpoint format.  A checkpoint of a tokens x cols matrix holds q, one byte
+ * per element, rows of MUON_CKPT_Q_PITCH(cols) bytes, and scale, one byte per
+ * block of MUON_CKPT_BLOCK = 32 columns of one row, rows of
+ * MUON_CKPT_SCALE_PITCH(cols) bytes.  An element stands for q * 2^(scale - 127),
+ * q an OCP e4m3 number (MUON_CKPT_E4M3) or a two's complement integer
+ * (MUON_CKPT_INT8).  Saving picks for each block the smallest exponent that
+ * brings its largest magnitude a to at most 448 (127), within [-117, 119]
+ * ([-117, 121]), and rounds x * 2^-e to the nearest q, ties to even; what the
+ * largest exponent cannot hold saturates.  A block with an infinity or a NaN
+ * gets scale 255 and reads as NaN throughout; a zero block gets exponent -117.
+ * Padding bytes are written as zero.  With a power of two as scale and at most
+ * 8 significant bits in q, every value read back is exact in bfloat16 and
+ * float32, so the weight gradient's products on bf16 matrix cores have no
+ * second rounding of the activation.
+ *
+ *  Memory   x, y, dy, dx: DEVICE pointers to tokens x cols matrices of `dtype`
+ *           with unit column stride.  Inputs x and dy have a row stride (ldx,
+ *           lddy, in elements, at least the row length), outputs y and dx are
+ *           contiguous.  gain, bias, dgain, dbias: cols elements of
+ *           `param_dtype`.  mean, rstd: float32, one per token.  q must be
+ *           16-byte and scale 4-byte aligned; every other pointer needs its
+ *           element's alignment only (aligned rows are faster for dy of the
+ *           weight gradient).  No output may overlap an input or another
+ *           output (a strided matrix counts from its first to its last
+ *           element); inputs may overlap each other.
+ *  Sizes    0 <= tokens <= MUON_MAX_TOKENS, 1 <= cols <= MUON_MAX_DIM (and rows
+ *           of the weight gradient).  tokens == 0 writes no per-token output;
+ *           parameter and weight gradients are then zero, or left as they are
+ *           when accumulating.
+ *  Stream, workspace, errors  as for the Muon entry points: everything that
+ *           the host can see is validated before anything is enqueued, no
+ *           allocation, no synchronisation; calls that overlap in time need
+ *           workspaces of their own.  Results are the same bits on every run:
+ *           all sums have a fixed order.
+ */
+#define MUON_MAX_TOKENS (((int64_t)1) << 30)
+#define MUON_CKPT_BLOCK 32
+#define MUON_CKPT_Q_PITCH(cols) (((cols) + 31) / 32 * 32)
+#define MUON_CKPT_SCALE_PITCH(cols) (((cols) + 127) / 128 * 4)
+enum { MUON_CKPT_E4M3 = 0, MUON_CKPT_INT8 = 1 };
+
+typedef struct muon_ckpt {
+  void* q;        /* [tokens][MUON_CKPT_Q_PITCH(cols)] bytes */
+  uint8_t* scale; /* [tokens][MUON_CKPT_SCALE_PITCH(cols)] bytes */
+  int64_t tokens;
+  int64_t cols;
+  int format;     /* MUON_CKPT_E4M3 or MUON_CKPT_INT8 */
+} muon_ckpt;
+
+/* Saves x (row stride ldx) into a checkpoint, or reads one back into a
+ * contiguous x of `dtype` (exact: no rounding). */
+int muon_checkpoint_save(const void* x, int64_t ldx, int dtype, const muon_ckpt* ckpt,
+                         void* stream);
+int muon_checkpoint_restore(const muon_ckpt* ckpt, void* x, int dtype, void* stream);
+
+/*
+ * Layer norm over the columns, statistics in float32 by two passes over the
+ * row in registers:
+ *   mean = sum_c x / cols,  rstd = 1 / sqrt(sum_c (x - mean)^2 / cols + eps)
+ *   y = (x - mean) * rstd * gain + bias        (bias may be NULL: none)
+ * eps must be finite and >= 0.  x_ckpt and y_ckpt (each may be NULL) also save
+ * x, or y as rounded to `dtype`, in the same pass.
+ */
+int muon_layernorm_forward(const void* x, int64_t ldx, const void* gain, const void* bias,
+                           int64_t tokens, int64_t cols, int dtype, int param_dtype, double eps,
+                           void* y, float* mean, float* rstd, const muon_ckpt* x_ckpt,
+                           const muon_ckpt* y_ckpt, void* stream);
+
+/*
+ * Its backward pass, from x or from a checkpoint of x (give one, the other
+ * NULL), with the forward's mean and rstd; xhat = (x - mean) * rstd:
+ *   dx     = rstd * (gain dy - avg_c(gain dy) - xhat avg_c(gain dy xhat))
+ *   dgain  = sum_t dy xhat,   dbias = sum_t dy        (dbias may be NULL)
+ * accumulate != 0 adds dgain and dbias to what their buffers hold (in float32,
+ * rounded once to param_dtype).
+ */
+size_t muon_layernorm_workspace_bytes(int64_t tokens, int64_t cols);
+int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                            const muon_ckpt* x_ckpt, const void* gain, const float* mean,
+                            const float* rstd, int64_t tokens, int64_t cols, int dtype,
+                            int param_dtype, void* dx, void* dgain, void* dbias, int accumulate,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Weight gradients of `count` linear layers y = x W^T (W rows x cols) whose
+ * inputs were saved in one checkpoint, in the stacked layout of muon_group:
+ *   G[e] = sum over the tokens t of e of  dy[t]^T x[t]         (rows x cols)
+ * dy: tokens x rows of `dtype` (row stride lddy); G: [count][rows][cols] of
+ * g_dtype.  offsets: DEVICE array of count + 1 int64, the tokens of matrix e
+ * are [offsets[e], offsets[e+1]); NULL with count == 1 takes every token.
+ * Offsets outside [0, tokens] are read as the nearest end of it and one smaller
+ * than those before it as the largest of them, so no offset leads outside the
+ * buffers; tokens before the first or from the last offset on belong to no
+ * matrix.  A matrix without tokens gets zeros.  accumulate != 0 adds to what G
+ * holds.  Products are exact in float32 (float32 dy is taken in three bf16
+ * parts, which hold its 24 bits) and accumulate in float32; G is rounded once.
+ */
+size_t muon_weight_grad_workspace_bytes(int64_t count, int64_t tokens, int64_t rows, int64_t cols);
+int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x,
+                     const int64_t* offsets, int64_t count, int64_t rows, void* G, int g_dtype,
+                     int accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Phase timing, for benchmarks and profiling.  While enabled (process-wide),

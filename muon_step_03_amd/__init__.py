@@ -1,5 +1,6 @@
-"""Muon optimizer step (and the AdamW step of the hybrid optimizer) for
-MI355X (gfx950): HIP kernels behind a C ABI.
+"""Muon optimizer step (with the AdamW step of the hybrid optimizer and the
+layer operators that make their gradients) for MI355X (gfx950): HIP kernels
+behind a C ABI.
 
 The HIP library (libmuon.so, built in-tree by ``muon_step_03_amd.build``) is
 loaded on first use; without it every entry point raises.
@@ -10,4 +11,8 @@ from .api import (  # noqa: F401
     muon_step_batched, muon_step_grouped, muon_step_grouped_noalloc, pointer_table,
     stacked_chunks, stacked_group, chunk_size, table_group, workspace_bytes,
     workspace_bytes_grouped,
+)
+from .layer_ops import (  # noqa: F401
+    ActCheckpoint, LayerNormOut, checkpoint_restore, checkpoint_save, layernorm_backward,
+    layernorm_forward, layernorm_workspace_bytes, weight_grad, weight_grad_workspace_bytes,
 )

@@ -32,6 +32,10 @@ MUON_GROUPS_PER_LAUNCH = 8
 MUON_ADAMW_MAX_ELEMENTS = 1 << 40
 MUON_ADAMW_TENSORS_PER_LAUNCH = 32
 MUON_NOALLOC_WORKSPACE_BYTES = 64 << 20
+MUON_MAX_TOKENS = 1 << 30
+MUON_CKPT_BLOCK = 32
+MUON_CKPT_E4M3 = 0
+MUON_CKPT_INT8 = 1
 
 # Every symbol include/muon.h declares.
 EXPORTS = (
@@ -39,6 +43,9 @@ EXPORTS = (
     "muon_step_batched", "muon_step_grouped", "muon_status_string", "muon_last_hip_error",
     "muon_profile_enable", "muon_profile_read", "muon_phase_name",
     "muon_adamw_step", "muon_adamw_step_grouped", "muon_step_grouped_noalloc",
+    "muon_checkpoint_save", "muon_checkpoint_restore", "muon_layernorm_forward",
+    "muon_layernorm_workspace_bytes", "muon_layernorm_backward",
+    "muon_weight_grad_workspace_bytes", "muon_weight_grad",
 )
 MUON_NUM_PHASES = 10
 
@@ -67,6 +74,26 @@ class AdamwTensor(ctypes.Structure):
         ("lr", ctypes.c_double),
         ("weight_decay", ctypes.c_double),
     ]
+
+
+class Ckpt(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("tokens", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("format", ctypes.c_int),
+    ]
+
+
+def ckpt_q_pitch(cols: int) -> int:
+    """Bytes per row of a checkpoint's q (MUON_CKPT_Q_PITCH)."""
+    return (cols + 31) // 32 * 32
+
+
+def ckpt_scale_pitch(cols: int) -> int:
+    """Bytes per row of a checkpoint's scales (MUON_CKPT_SCALE_PITCH)."""
+    return (cols + 127) // 128 * 4
 
 
 _lib = None
@@ -119,6 +146,25 @@ def lib():
                                           ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                           ctypes.c_int64, ctypes.c_void_p]
     L.muon_adamw_step_grouped.restype = ctypes.c_int
+    p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    ck = ctypes.POINTER(Ckpt)
+    L.muon_checkpoint_save.argtypes = [p, i64, i32, ck, p]
+    L.muon_checkpoint_save.restype = i32
+    L.muon_checkpoint_restore.argtypes = [ck, p, i32, p]
+    L.muon_checkpoint_restore.restype = i32
+    L.muon_layernorm_forward.argtypes = [p, i64, p, p, i64, i64, i32, i32, ctypes.c_double,
+                                         p, p, p, ck, ck, p]
+    L.muon_layernorm_forward.restype = i32
+    L.muon_layernorm_workspace_bytes.argtypes = [i64, i64]
+    L.muon_layernorm_workspace_bytes.restype = ctypes.c_size_t
+    L.muon_layernorm_backward.argtypes = [p, i64, p, i64, ck, p, p, p, i64, i64, i32, i32,
+                                          p, p, p, i32, p, ctypes.c_size_t, p]
+    L.muon_layernorm_backward.restype = i32
+    L.muon_weight_grad_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.muon_weight_grad_workspace_bytes.restype = ctypes.c_size_t
+    L.muon_weight_grad.argtypes = [p, i64, i32, ck, p, i64, i64, p, i32, i32, p,
+                                   ctypes.c_size_t, p]
+    L.muon_weight_grad.restype = i32
     L.muon_phase_name.argtypes = [ctypes.c_int]
     L.muon_phase_name.restype = ctypes.c_char_p
     _lib = L

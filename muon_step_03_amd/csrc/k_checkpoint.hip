@@ -1,0 +1,118 @@
+// Activation checkpoints: x -> 8-bit q with one power-of-two scale per block of
+// 32 columns, and back.  HBM-bound: 2 (or 4) bytes in and 33/32 out per
+// element, and the reverse.
+//
+// A vector is 16 bytes of x (8 bf16 or 4 float32), so 4 or 8 consecutive lanes
+// hold a block and find its largest magnitude with two or three lane exchanges.
+#include "layer_internal.h"
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPerThread = 4;   // vectors in flight per thread
+
+// Vectors per row, padding included: whole scale words, so that the lanes
+// past the row write the padding of q and scale.
+__host__ __device__ __forceinline__ uint32_t vecs_per_row(const Ckpt& c, int n) {
+  return uint32_t(c.s_pitch * MUON_CKPT_BLOCK / n);
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void save_kernel(const void* x, int64_t ldx, Ckpt c,
+                                                        int64_t tokens, int cols) {
+  using R = RowVec<BF16>;
+  constexpr int N = R::N;
+  const uint32_t vpr = vecs_per_row(c, N);
+  const int64_t total = tokens * int64_t(vpr);
+  for (int64_t base = int64_t(blockIdx.x) * (kThreads * kPerThread); base < total;
+       base += int64_t(gridDim.x) * (kThreads * kPerThread)) {
+    const int64_t row0 = base / vpr;
+    const uint32_t rem = uint32_t(base - row0 * vpr);
+    float v[kPerThread][N];
+    int64_t row[kPerThread];
+    int col[kPerThread];
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const uint32_t at = rem + j * kThreads + threadIdx.x;
+      const uint32_t r = at / vpr;
+      row[j] = row0 + r;
+      col[j] = int((at - r * vpr) * N);
+      if (row[j] < tokens) {
+        load_vec<BF16>(static_cast<const typename R::T*>(x) + row[j] * ldx, col[j], cols, v[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[j][i] = 0.f;
+      }
+    }
+    // blocks of a row never straddle a wave (vpr is a multiple of 16), and the
+    // lanes of one block lie in one row: they all pass the test below together
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j)
+      if (row[j] < tokens) ckpt_store<N>(c, row[j], col[j], cols, v[j]);
+  }
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void restore_kernel(Ckpt c, void* x, int64_t tokens,
+                                                           int cols) {
+  using R = RowVec<BF16>;
+  constexpr int N = R::N;
+  const uint32_t vpr = uint32_t((cols + N - 1) / N);
+  const int64_t total = tokens * int64_t(vpr);
+  for (int64_t base = int64_t(blockIdx.x) * (kThreads * kPerThread); base < total;
+       base += int64_t(gridDim.x) * (kThreads * kPerThread)) {
+    const int64_t row0 = base / vpr;
+    const uint32_t rem = uint32_t(base - row0 * vpr);
+    float v[kPerThread][N];
+    int64_t row[kPerThread];
+    int col[kPerThread];
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const uint32_t at = rem + j * kThreads + threadIdx.x;
+      const uint32_t r = at / vpr;
+      row[j] = row0 + r;
+      col[j] = int((at - r * vpr) * N);
+      if (row[j] < tokens) ckpt_load<N>(c, row[j], col[j], v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j)
+      if (row[j] < tokens)
+        store_vec<BF16>(static_cast<typename R::T*>(x) + row[j] * cols, col[j], cols, v[j]);
+  }
+}
+
+// Enough blocks to fill the chip several times over; larger inputs loop.
+unsigned grid_for(int64_t vectors) {
+  const int64_t b = (vectors + kThreads * kPerThread - 1) / (kThreads * kPerThread);
+  return unsigned(b < 65536 ? b : 65536);
+}
+
+}  // namespace
+
+hipError_t launch_ckpt_save(const void* x, int64_t ldx, bool bf16, const Ckpt& c, int64_t tokens,
+                            int cols, hipStream_t s) {
+  const int64_t vecs = tokens * int64_t(vecs_per_row(c, bf16 ? 8 : 4));
+  if (bf16)
+    hipLaunchKernelGGL(save_kernel<true>, dim3(grid_for(vecs)), dim3(kThreads), 0, s, x, ldx, c,
+                       tokens, cols);
+  else
+    hipLaunchKernelGGL(save_kernel<false>, dim3(grid_for(vecs)), dim3(kThreads), 0, s, x, ldx, c,
+                       tokens, cols);
+  return hipGetLastError();
+}
+
+hipError_t launch_ckpt_restore(const Ckpt& c, void* x, bool bf16, int64_t tokens, int cols,
+                               hipStream_t s) {
+  const int n = bf16 ? 8 : 4;
+  const int64_t vecs = tokens * int64_t((cols + n - 1) / n);
+  if (bf16)
+    hipLaunchKernelGGL(restore_kernel<true>, dim3(grid_for(vecs)), dim3(kThreads), 0, s, c, x,
+                       tokens, cols);
+  else
+    hipLaunchKernelGGL(restore_kernel<false>, dim3(grid_for(vecs)), dim3(kThreads), 0, s, c, x,
+                       tokens, cols);
+  return hipGetLastError();
+}
+
+}  // namespace muon

@@ -758,6 +758,20 @@ void* scratch_on_current_device() {
 
 }  // namespace
 
+namespace muon {
+
+void note_hip_error(hipError_t e) { g_last_hip_error = int(e); }
+bool debug_sync_enabled() { return debug_sync(); }
+int compute_units() { return 8 * cus_per_xcd(); }
+void trace_push(const char* name) {
+  if (const Roctx* t = roctx()) t->push(name);
+}
+void trace_pop() {
+  if (const Roctx* t = roctx()) t->pop();
+}
+
+}  // namespace muon
+
 extern "C" {
 
 int muon_adamw_step(void* P, const void* G, float* m, float* v, int64_t n, int dtype, double lr,
