@@ -351,7 +351,7 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
                             void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Weight gradients of `count` linear layers y = x W^T (W rows x cols) whose
+ * Weight gradients of `count` (<= MUON_WEIGHT_GRAD_MAX_COUNT) linear layers y = x W^T (W rows x cols) whose
  * inputs were saved in one checkpoint, in the stacked layout of muon_group:
  *   G[e] = sum over the tokens t of e of  dy[t]^T x[t]         (rows x cols)
  * dy: tokens x rows of `dtype` (row stride lddy); G: [count][rows][cols] of
@@ -364,6 +364,7 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
  * holds.  Products are exact in float32 (float32 dy is taken in three bf16
  * parts, which hold its 24 bits) and accumulate in float32; G is rounded once.
  */
+#define MUON_WEIGHT_GRAD_MAX_COUNT (1 << 20)
 size_t muon_weight_grad_workspace_bytes(int64_t count, int64_t tokens, int64_t rows, int64_t cols);
 int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x,
                      const int64_t* offsets, int64_t count, int64_t rows, void* G, int g_dtype,

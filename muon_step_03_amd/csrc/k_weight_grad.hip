@@ -15,6 +15,7 @@
 // one of several leaves float32 tiles that the join kernel adds in order: no
 // atomics, the same bits on every run.
 #include <algorithm>
+#include <type_traits>
 
 #include "lds_tiles.h"
 #include "layer_internal.h"
@@ -23,102 +24,242 @@ namespace muon {
 namespace {
 
 constexpr int BM = 128, BN = 128, BK = 32;   // rows of G, columns of G, tokens
-constexpr int NT = 256;                      // 2 x 2 waves of 64 x 64
-constexpr int kTile = BM * BN;
+constexpr int kThreads = 256;                // 2 x 2 waves of 64 x 64
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
+// A piece: tokens [begin, end) of matrix e; slot: its place among the partial
+// sums (parts > 1).  In the table of a ragged call, e < 0 marks no piece.
 struct Piece {
-  int e;             // matrix
-  int begin, end;    // tokens
-  int parts;         // pieces of its matrix
-  int64_t slot;      // its place among the partial sums (parts > 1)
+  int e, begin, end, parts;
+  int64_t slot;
+  int64_t pad_;
 };
+static_assert(sizeof(Piece) == kWeightGradPieceBytes, "size of the table");
+// A matrix of several pieces, for the join.
+struct Split {
+  int e, parts;
+  int64_t slot;
+};
+static_assert(sizeof(Split) == kWeightGradSplitBytes, "size of the table");
 
-// Piece number `want`, or the matrix number `want` when BY_MATRIX (begin and
-// end are then those of its first piece).  False past the last.  Every wave
-// scans the offsets 64 at a time; begin offsets are read as the largest
-// offset so far, clamped to [0, tokens], so that no piece leaves the buffers
-// and their number is bounded whatever the offsets hold.
-template <bool BY_MATRIX>
-__device__ __forceinline__ bool find_piece(const WeightGrad& p, int64_t want, Piece& out) {
-  const int64_t C = p.chunk;
-  if (!p.offsets) {
-    const int64_t parts = p.tokens > C ? (p.tokens + C - 1) / C : 1;
-    if (want >= (BY_MATRIX ? 1 : parts)) return false;
-    out.e = 0;
-    out.begin = int(BY_MATRIX ? 0 : want * C);
-    out.end = int(out.begin + C < p.tokens ? out.begin + C : p.tokens);
-    out.parts = int(parts);
-    out.slot = BY_MATRIX ? 0 : want;
-    return true;
-  }
-  const int lane = threadIdx.x & 63;
+// Ragged calls: the pieces of all matrices and the list of the split ones,
+// from the offsets on the device.  One block; a thread takes a matrix.  The
+// offsets are clamped to [0, tokens] and read as the largest so far, so that
+// no piece leaves the buffers and their number is bounded whatever the offsets
+// hold.  A matrix's tokens are shared evenly between its pieces, in whole
+// steps.  Up to 1024 matrices, pieces are put in order of their length,
+// longest first: blocks start in this order, so that all end together.  Up to
+// 64 matrices need one wave (NT = 64).
+constexpr int kPlanThreads = 1024;
+template <int NT>
+__global__ __launch_bounds__(NT) void plan_kernel(const WeightGrad p) {
+  constexpr int WAVES = NT / 64;
+  __shared__ int wave_top[WAVES], wave_n[WAVES], wave_m[WAVES], wave_s[WAVES];
+  __shared__ int keys[NT], counts[NT];
+  Piece* table = static_cast<Piece*>(p.table);
+  Split* splits = reinterpret_cast<Split*>(table + p.pieces);
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int T = int(p.tokens);
   auto clamp = [&](int64_t v) { return int(v < 0 ? 0 : v > T ? T : v); };
-  int top = clamp(p.offsets[0]);   // largest offset before this group of 64
-  int64_t pieces = 0, slots = 0;
-  for (int base = 0; base < p.count; base += 64) {
-    const bool in = base + lane < p.count;
-    int hi = in ? clamp(p.offsets[base + lane + 1]) : 0;
+  int top = clamp(p.offsets[0]);
+  int pieces = 0, slots = 0, split = 0;   // of the matrices before this group
+  for (int base = 0; base < p.count; base += NT) {
+    const int e = base + t;
+    const bool in = e < p.count;
+    // end of every matrix: the largest offset up to it
+    int hi = in ? clamp(p.offsets[e + 1]) : 0;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const int o = __shfl_up(hi, off, 64);
       if (lane >= off && o > hi) hi = o;
     }
-    hi = hi > top ? hi : top;
+    if (lane == 63) wave_top[wave] = hi;
+    __syncthreads();
+    int before = top;
+    for (int w = 0; w < wave; ++w) before = before > wave_top[w] ? before : wave_top[w];
+    hi = hi > before ? hi : before;
     int lo = __shfl_up(hi, 1, 64);
-    if (lane == 0) lo = top;
-    const uint32_t len = uint32_t(hi - lo);
-    const int n = !in ? 0 : len <= p.chunk ? 1 : int((len + p.chunk - 1) / p.chunk);
-    const int m = n > 1 ? n : 0;
-    int sn = n, sm = m;   // inclusive sums
+    if (lane == 0) lo = before;
+    for (int w = 0; w < WAVES; ++w) top = top > wave_top[w] ? top : wave_top[w];
+    // pieces, slots and split matrices before this one
+    const int len = hi - lo, chunk = int(p.chunk);
+    const int n = !in ? 0 : len <= chunk ? 1 : (len - 1) / chunk + 1;
+    const int m = n > 1 ? n : 0, d = n > 1 ? 1 : 0;
+    int sn = n, sm = m, sd = d;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int a = __shfl_up(sn, off, 64), b = __shfl_up(sm, off, 64);
+      const int x = __shfl_up(sn, off, 64), y = __shfl_up(sm, off, 64), z = __shfl_up(sd, off, 64);
       if (lane >= off) {
-        sn += a;
-        sm += b;
+        sn += x;
+        sm += y;
+        sd += z;
       }
     }
-    const bool hit = BY_MATRIX ? in && base + lane == want
-                               : want >= pieces + sn - n && want < pieces + sn;
-    const uint64_t mask = __ballot(hit);
-    if (mask) {
-      const int src = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)mask) - 1);
-      const int first = __builtin_amdgcn_readlane(lo, src);
-      const int last = __builtin_amdgcn_readlane(hi, src);
-      const int before = __builtin_amdgcn_readlane(sn - n, src);
-      const int j = BY_MATRIX ? 0 : int(want - pieces) - before;
-      out.e = base + src;
-      out.begin = first + j * int(p.chunk);
-      out.end = last - out.begin > int(p.chunk) ? out.begin + int(p.chunk) : last;
-      out.parts = __builtin_amdgcn_readlane(n, src);
-      out.slot = slots + __builtin_amdgcn_readlane(sm - m, src) + j;
-      return true;
+    if (lane == 63) {
+      wave_n[wave] = sn;
+      wave_m[wave] = sm;
+      wave_s[wave] = sd;
     }
-    pieces += __builtin_amdgcn_readlane(sn, 63);
-    slots += __builtin_amdgcn_readlane(sm, 63);
-    top = __builtin_amdgcn_readlane(hi, 63);
+    const int share = n > 1 ? ((len + n - 1) / n + BK - 1) / BK * BK : len;
+    keys[t] = share;
+    counts[t] = n;
+    __syncthreads();
+    int first = pieces + sn - n, slot = slots + sm - m, at = split + sd - d;
+    for (int w = 0; w < wave; ++w) {
+      first += wave_n[w];
+      slot += wave_m[w];
+      at += wave_s[w];
+    }
+    if (p.count <= NT) {
+      first = 0;
+      if constexpr (NT == 64) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {   // lanes past the last matrix have no pieces
+          const int kj = __builtin_amdgcn_readlane(share, j), nj = __builtin_amdgcn_readlane(n, j);
+          first += kj > share || (kj == share && j < t) ? nj : 0;
+        }
+      } else {
+        for (int j = 0; j < p.count; ++j)
+          first += keys[j] > share || (keys[j] == share && j < t) ? counts[j] : 0;
+      }
+    }
+    for (int j = 0; j < n; ++j) {
+      Piece pc{};
+      pc.e = e;
+      pc.begin = j * share < len ? lo + j * share : hi;
+      pc.end = hi - pc.begin > share ? pc.begin + share : hi;
+      pc.parts = n;
+      pc.slot = slot + j;
+      table[first + j] = pc;
+    }
+    if (d) splits[at] = Split{e, n, slot};
+    for (int w = 0; w < WAVES; ++w) {
+      pieces += wave_n[w];
+      slots += wave_m[w];
+      split += wave_s[w];
+    }
+    __syncthreads();
   }
-  return false;
+  for (int64_t i = pieces + t; i < p.pieces; i += NT) table[i].e = -1;
+  if (t == 0) splits[p.count] = Split{split, 0, 0};   // their number
 }
 
-// Four consecutive columns of one row of a matrix's gradient.
-__device__ __forceinline__ void store_g(const WeightGrad& p, int64_t base, int row, int col,
-                                        f32x4_t v) {
-  if (row >= p.rows) return;
-  const int64_t at = base + int64_t(row) * p.cols + col;
+// The piece and tile of block `b`.  The hardware deals blocks to the 8 XCDs in
+// turn; tiles that share operands are put on one XCD, which has an L2 of its
+// own: without offsets XCD x takes a contiguous eighth of all tiles, with
+// them the tiles of a piece (at most 32 at a time, an XCD's compute units) go
+// to the XCDs in turn.
+__device__ __forceinline__ bool find_piece(const WeightGrad& p, uint32_t b, uint32_t tiles,
+                                           Piece& out, int& tile) {
+  const uint32_t turn = b >> 3, pieces = uint32_t(p.pieces);
+  if (!p.offsets) {
+    const uint32_t per = (pieces * tiles + 7) / 8, id = (b & 7) * per + turn;
+    if (turn >= per || id >= pieces * tiles) return false;
+    const uint32_t want = id / tiles;
+    tile = int(id - want * tiles);
+    out.e = 0;
+    out.begin = int(want * p.chunk);
+    out.end = int(out.begin + p.chunk < p.tokens ? out.begin + p.chunk : p.tokens);
+    out.parts = int(pieces);
+    out.slot = want;
+    return true;
+  }
+  const uint32_t deal = tiles < 32 ? tiles : 32;
+  const uint32_t id = (turn / deal * 8 + (b & 7)) * deal + turn % deal;
+  const uint32_t want = id / tiles;
+  tile = int(id - want * tiles);
+  if (want >= pieces) return false;
+  const Piece pc = static_cast<const Piece*>(p.table)[want];
+  out.e = __builtin_amdgcn_readfirstlane(pc.e);
+  out.begin = __builtin_amdgcn_readfirstlane(pc.begin);
+  out.end = __builtin_amdgcn_readfirstlane(pc.end);
+  out.parts = __builtin_amdgcn_readfirstlane(pc.parts);
+  out.slot = __builtin_amdgcn_readfirstlane(int(pc.slot));
+  return out.e >= 0;
+}
+
+// Tile number -> tile row and column: groups of 8 tile rows, columns first
+// within a group, so that 32 consecutive tiles (an XCD's compute units) read
+// 8 column strips of dy and 4 of x.
+__device__ __forceinline__ void place_tile(int tile, int tiles_m, int tiles_n, int& ti, int& tj) {
+  const int group = tile / (8 * tiles_n), r = tile - group * 8 * tiles_n;
+  const int rows = tiles_m - group * 8 < 8 ? tiles_m - group * 8 : 8;
+  tj = r / rows;
+  ti = group * 8 + r - tj * rows;
+}
+
+// Eight consecutive columns of one row: into the gradient, or (to != null)
+// into a row-major float32 matrix of partial sums.
+__device__ __forceinline__ void store_row8(const WeightGrad& p, float* to, int64_t base, int row,
+                                           int col, f32x4_t lo, f32x4_t hi) {
+  if (row >= p.rows || col >= p.cols) return;
+  const int64_t at = int64_t(row) * p.cols + col;
+  float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (col + i >= p.cols) break;
-    if (p.g_bf16) {
-      uint16_t* g = static_cast<uint16_t*>(p.G) + at + i;
-      *g = f2bf(p.accumulate ? bf2f(*g) + v[i] : v[i]);
-    } else {
-      float* g = static_cast<float*>(p.G) + at + i;
-      *g = p.accumulate ? *g + v[i] : v[i];
+    v[i] = lo[i];
+    v[4 + i] = hi[i];
+  }
+  const int left = p.cols - col;
+  if (to) {
+    store_vec<false>(to + at, 0, left, v);
+    store_vec<false>(to + at, 4, left, v + 4);
+    return;
+  }
+  float old[8];
+  if (p.g_bf16) {
+    uint16_t* g = static_cast<uint16_t*>(p.G) + base + at;
+    if (p.accumulate) {
+      load_vec<true>(g, 0, left, old);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += old[i];
     }
+    store_vec<true>(g, 0, left, v);
+  } else {
+    float* g = static_cast<float*>(p.G) + base + at;
+    if (p.accumulate) {
+      load_vec<false>(g, 0, left, old);
+      load_vec<false>(g, 4, left, old + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += old[i];
+    }
+    store_vec<false>(g, 0, left, v);
+    store_vec<false>(g, 4, left, v + 4);
+  }
+}
+
+// Writes a wave's 32 MI x 64 accumulators (rows from i0, columns from j0)
+// through a window of LDS of its own, 32 rows at a time, so that lanes store
+// whole runs of a row.  Lane l, register 4 g + i of a 32 x 32 block holds row
+// l % 32, column 8 g + 4 (l / 32) + i.  A pitch of 68 floats spreads the
+// 16-byte writes of 16 rows over all banks.
+constexpr int kWindow = 32 * 68 * 4;   // bytes per wave
+template <int MI>
+__device__ __forceinline__ void store_tile(const WeightGrad& p, const Piece& pc, int i0, int j0,
+                                           const f32x16_t (&acc)[MI][2], LDS_AS char* window,
+                                           int lane) {
+  const int64_t size = int64_t(p.rows) * p.cols;
+  float* to = pc.parts > 1 ? p.partial + pc.slot * size : nullptr;
+  LDS_AS float* w = (LDS_AS float*)window;
+#pragma unroll
+  for (int a = 0; a < MI; ++a) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *(LDS_AS f32x4_t*)(w + (lane & 31) * 68 + b * 32 + 8 * g + 4 * (lane >> 5)) =
+            f32x4_t{acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2],
+                    acc[a][b][4 * g + 3]};
+    wave_lds_sync();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = r * 8 + (lane >> 3), col = (lane & 7) * 8;
+      const f32x4_t lo = *(const LDS_AS f32x4_t*)(w + row * 68 + col);
+      const f32x4_t hi = *(const LDS_AS f32x4_t*)(w + row * 68 + col + 4);
+      store_row8(p, to, pc.e * size, i0 + a * 32 + row, j0 + col, lo, hi);
+    }
+    wave_lds_sync();
   }
 }
 
@@ -136,20 +277,21 @@ __device__ __forceinline__ int tile_at(int k, int chunk) {
 }
 
 template <bool BF16>
-__global__ __launch_bounds__(NT, 2) void weight_grad_kernel(const WeightGrad p, int tiles_n,
-                                                            int tiles) {
+__global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGrad p, int tiles_m,
+                                                            int tiles_n) {
   constexpr int P = BF16 ? 1 : 3;            // bf16 parts of dy
   constexpr int PLANE = BK * BM * 2;         // bytes
   constexpr int STAGE = (P + 1) * PLANE;
   static_assert(BM == BN, "one tile layout");
-  __shared__ __attribute__((aligned(1024))) char smem_raw[2 * STAGE];
+  constexpr int WINDOWS = kThreads / 64 * kWindow;   // of the epilogue
+  __shared__ __attribute__((aligned(1024))) char smem_raw[2 * STAGE > WINDOWS ? 2 * STAGE : WINDOWS];
   LDS_AS char* smem = (LDS_AS char*)smem_raw;
 
-  const int64_t number = blockIdx.x / unsigned(tiles);
-  const int tile = int(blockIdx.x - number * tiles);
   Piece pc;
-  if (!find_piece<false>(p, number, pc)) return;
-  const int i0 = tile / tiles_n * BM, j0 = tile % tiles_n * BN;
+  int tile, ti, tj;
+  if (!find_piece(p, blockIdx.x, tiles_m * tiles_n, pc, tile)) return;
+  place_tile(tile, tiles_m, tiles_n, ti, tj);
+  const int i0 = ti * BM, j0 = tj * BN;
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -261,95 +403,441 @@ __global__ __launch_bounds__(NT, 2) void weight_grad_kernel(const WeightGrad p, 
     __syncthreads();
   }
 
-  // Lane l, register 4 g + i of a 32 x 32 block: row l % 32, column 8 g + 4 (l / 32) + i.
-  const bool direct = pc.parts == 1;
-  if (direct && steps == 0 && p.accumulate) return;
-  const int64_t base = int64_t(pc.e) * p.rows * p.cols;
-  float* part = p.partial + (pc.slot * tiles + tile) * int64_t(kTile);
-#pragma unroll
-  for (int a = 0; a < 2; ++a)
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4_t v = {acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2],
-                           acc[a][b][4 * g + 3]};
-        if (direct)
-          store_g(p, base, i0 + wm * 64 + a * 32 + (lane & 31),
-                  j0 + wn * 64 + b * 32 + 8 * g + 4 * (lane >> 5), v);
-        else
-          *reinterpret_cast<f32x4_t*>(part + ((((a * 2 + b) * 4 + g) * 4 + wave) * 64 + lane) * 4) = v;
-      }
+  if (pc.parts == 1 && steps == 0 && p.accumulate) return;
+  store_tile<2>(p, pc, i0 + wm * 64, j0 + wn * 64, acc, smem + wave * kWindow, lane);
 }
 
-// Adds the partial tiles of matrices with several pieces, one 32 x 32 block
-// of each wave's tile per block.
-__global__ __launch_bounds__(NT) void join_kernel(const WeightGrad p, int tiles_n, int tiles) {
-  const int64_t id = blockIdx.x;
-  const int ab = int(id & 3);
-  const int tile = int((id >> 2) % tiles);
-  Piece pc;
-  if (!find_piece<true>(p, (id >> 2) / tiles, pc) || pc.parts == 1) return;
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int wm = wave >> 1, wn = wave & 1, a = ab >> 1, b = ab & 1;
-  const int64_t base = int64_t(pc.e) * p.rows * p.cols;
-  f32x4_t sum[4] = {};
-  for (int j = 0; j < pc.parts; ++j) {
-    const float* part = p.partial + ((pc.slot + j) * tiles + tile) * int64_t(kTile);
+// ------------------------------------------------------ bf16 dy in aligned rows
+// Tiles of 256 x 256, one block of 8 waves per CU, waves of 128 x 64.  Steps of
+// 32 tokens: dy, the 8-bit x and its scales go straight to LDS; each wave turns
+// the x bytes that it loaded itself into its part of the bf16 tile two steps
+// ahead, between its matrix instructions.
+struct Wide {
+  static constexpr int NW = 8, BM = 256, BN = 256, WGN = 4, MI = 4, NI = 2;
+  static constexpr int YS = 4, XS = 4, QS = 2;   // buffers of dy, bf16 x, x bytes with scales
+  static constexpr int Y_BYTES = BK * BM * 2, X_BYTES = BK * BN * 2;
+  static constexpr int Q_BYTES = BK * BN, QW_BYTES = Q_BYTES + NW * 256;
+  static constexpr int Y_INSTR = Y_BYTES / NW / WAVE_BYTES;
+  static constexpr int X_AT = YS * Y_BYTES, Q_AT = X_AT + XS * X_BYTES;
+  static constexpr int LDS = Q_AT + QS * QW_BYTES;
+  static_assert(Q_BYTES == NW * WAVE_BYTES, "one x load per wave");
+  static_assert(QW_BYTES <= X_BYTES, "x bytes of the first steps in unused x tiles");
+  static_assert(LDS >= NW * kWindow && LDS <= 160 * 1024, "LDS");
+};
+
+// Byte address of the 8 columns `chunk` of token row k in a [BK][W] tile of
+// bf16 x.  On top of the swizzle that the fragment reads need, the upper half
+// of a 512-byte row is shifted by a chunk: lanes that write every other chunk
+// of a row then use all banks once.
+template <int W>
+__device__ __forceinline__ int x_at(int k, int chunk) {
+  return k * (W * 2) + ((chunk ^ gswz(k) ^ ((chunk >> 4) & 1)) << 4);
+}
+// Fragment of a tile laid out so: lane l gets column nb + l % 32, tokens
+// kb + 8 (l / 32) .. + 7 (lds_frag_xT with the shift).
+template <int W>
+__device__ __forceinline__ bf16x8_t frag_x(const LDS_AS char* tile, int kb, int nb, int lane) {
+  const int s = lane & 15;
+  const int n = nb + 16 * ((lane >> 4) & 1) + 4 * (s & 3);
+  const int k = kb + 8 * (lane >> 5) + (s >> 2);
+  const LDS_AS char* p0 = tile + x_at<W>(k, n >> 3) + (n & 7) * 2;
+  const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4_t*)p0);
+  const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4_t*)(p0 + 4 * W * 2));
+  const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// Sixteen checkpoint bytes -> sixteen bf16, exact; a marked block gives NaN.
+template <int FMT>
+__device__ __forceinline__ void unpack16(u32x4_t q, int byte, uint32_t (&o)[8]) {
+  if constexpr (FMT == MUON_CKPT_E4M3) {
+    // the conversion scales by the exponent of `up`, 255 giving NaN
+    const float up = __uint_as_float(uint32_t(byte) << 23);
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-      sum[g] += *reinterpret_cast<const f32x4_t*>(part + (((ab * 4 + g) * 4 + wave) * 64 + lane) * 4);
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], up, false));
+      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], up, true));
+    }
+  } else {
+    // bytes offset to unsigned, the offset taken off again in the scaling
+    const float up = ckpt_up(byte), off = -128.f * up;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = q[i] ^ 0x80808080u;
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = __builtin_fmaf(float((w >> (8 * j)) & 0xffu), up, off);
+      o[2 * i] = f2bf2(v[0], v[1]);
+      o[2 * i + 1] = f2bf2(v[2], v[3]);
+    }
   }
+}
+
+template <int FMT>
+__global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
+    const WeightGrad p, int tiles_m, int tiles_n) {
+  using C = Wide;
+  constexpr int BM = C::BM, BN = C::BN, MI = C::MI, NI = C::NI;
+  __shared__ __attribute__((aligned(1024))) char smem_raw[C::LDS];
+  LDS_AS char* smem = (LDS_AS char*)smem_raw;
+  const uint32_t smem_base = uint32_t(reinterpret_cast<uintptr_t>(smem));
+
+  Piece pc;
+  int tile, ti, tj;
+  if (!find_piece(p, blockIdx.x, tiles_m * tiles_n, pc, tile)) return;
+  place_tile(tile, tiles_m, tiles_n, ti, tj);
+  const int i0 = ti * BM, j0 = tj * BN;
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / C::WGN, wn = wave % C::WGN;
+  const int len = pc.end - pc.begin;
+  const int steps = (len + BK - 1) / BK;
+  const int last = len - (steps - 1) * BK;   // tokens of the last step
+
+  // Addresses of this lane's loads within a step.  Columns past a row's end
+  // read its last ones instead (they only reach elements of G that are not
+  // stored), tokens past the end the last token (their dy is zeroed below).
+  int y_k[C::Y_INSTR];
+  uint32_t y_off[C::Y_INSTR];
+  const uint32_t y_ld = uint32_t(p.lddy) * 2;
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
-    store_g(p, base, tile / tiles_n * BM + wm * 64 + a * 32 + (lane & 31),
-            tile % tiles_n * BN + wn * 64 + b * 32 + 8 * g + 4 * (lane >> 5), sum[g]);
+  for (int i = 0; i < C::Y_INSTR; ++i) {
+    constexpr int CPR = BM / 8;   // chunks per token row
+    const int at = (wave * C::Y_INSTR + i) * 64 + lane;
+    y_k[i] = at / CPR;
+    const int col = i0 + ((at % CPR) ^ gswz(y_k[i])) * 8;
+    y_off[i] = uint32_t(y_k[i]) * y_ld + uint32_t(col < p.rows ? col : p.rows - 8) * 2;
+  }
+  constexpr int XL = BN / 16;     // lanes per token row of x
+  const int x_k = wave * (64 / XL) + lane / XL, x_c = lane % XL;
+  const int x_col = j0 + x_c * 16, s_col = (j0 / MUON_CKPT_BLOCK) + (x_c / 2 & ~3);
+  const uint32_t q_ld = uint32_t(p.x.q_pitch), s_ld = uint32_t(p.x.s_pitch);
+  const uint32_t q_off = uint32_t(x_k) * q_ld + (x_col < int(q_ld) ? x_col : int(q_ld) - 16);
+  const uint32_t s_off = uint32_t(x_k) * s_ld + (s_col < int(s_ld) ? s_col : int(s_ld) - 4);
+  const char* y_base = static_cast<const char*>(p.dy) + int64_t(pc.begin) * y_ld;
+  const char* q_base = reinterpret_cast<const char*>(p.x.q) + int64_t(pc.begin) * q_ld;
+  const char* s_base = reinterpret_cast<const char*>(p.x.scale) + int64_t(pc.begin) * s_ld;
+
+  // Loads of step k: dy into buffer J; the bytes and scales of x to byte `at` of
+  // LDS.  END: k may be the last step.
+  auto issue_y = [&](auto buf, auto end, int i, int k) {
+    constexpr int J = decltype(buf)::value;
+    uint32_t off = y_off[i];
+    if (decltype(end)::value && k == steps - 1 && y_k[i] >= last)
+      off -= uint32_t(y_k[i] - (last - 1)) * y_ld;
+    dma16(off, y_base + int64_t(k) * BK * y_ld,
+          smem_base + J * C::Y_BYTES + (wave * C::Y_INSTR + i) * WAVE_BYTES);
+  };
+  auto issue_q = [&](auto end, int at, int k) {
+    uint32_t off = q_off;
+    if (decltype(end)::value && k == steps - 1 && x_k >= last) off -= uint32_t(x_k - (last - 1)) * q_ld;
+    dma16(off, q_base + int64_t(k) * BK * q_ld, smem_base + at + wave * WAVE_BYTES);
+  };
+  auto issue_s = [&](auto end, int at, int k) {
+    uint32_t off = s_off;
+    if (decltype(end)::value && k == steps - 1 && x_k >= last) off -= uint32_t(x_k - (last - 1)) * s_ld;
+    dma4(off, s_base + int64_t(k) * BK * s_ld, smem_base + at + C::Q_BYTES + wave * 256);
+  };
+  // This wave's x bytes of a step, and its part of their bf16 tile X.
+  u32x4_t q;
+  uint32_t sw;
+  auto read_q = [&](int at) {
+    q = *reinterpret_cast<const LDS_AS u32x4_t*>(smem + at + wave * WAVE_BYTES + lane * 16);
+    sw = *reinterpret_cast<const LDS_AS uint32_t*>(smem + at + C::Q_BYTES + wave * 256 + lane * 4);
+  };
+  uint32_t o[8];
+  auto unpack = [&]() { unpack16<FMT>(q, (sw >> (8 * ((x_c / 2) & 3))) & 0xff, o); };
+  auto write_x = [&](auto tile_x) {
+    LDS_AS char* x = smem + C::X_AT + decltype(tile_x)::value * C::X_BYTES;
+    *reinterpret_cast<LDS_AS u32x4_t*>(x + x_at<BN>(x_k, 2 * x_c)) = u32x4_t{o[0], o[1], o[2], o[3]};
+    *reinterpret_cast<LDS_AS u32x4_t*>(x + x_at<BN>(x_k, 2 * x_c + 1)) = u32x4_t{o[4], o[5], o[6], o[7]};
+  };
+  // dy of the tokens past the end, in buffer J of the last step: zero.
+  auto zero_tail = [&](auto buf) {
+#pragma unroll
+    for (int i = 0; i < C::Y_INSTR; ++i)
+      if (y_k[i] >= last)
+        *reinterpret_cast<LDS_AS u32x4_t*>(smem + decltype(buf)::value * C::Y_BYTES +
+                                           (wave * C::Y_INSTR + i) * WAVE_BYTES + lane * 16) =
+            u32x4_t{0, 0, 0, 0};
+  };
+
+  f32x16_t acc[MI][NI];
+#pragma unroll
+  for (int a = 0; a < MI; ++a)
+#pragma unroll
+    for (int b = 0; b < NI; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+
+  bf16x8_t yf[2][MI], xf[2][NI];
+  auto frags = [&](auto buf, auto tile_x, int ks) {
+    constexpr int J = decltype(buf)::value, X = decltype(tile_x)::value;
+#pragma unroll
+    for (int a = 0; a < MI; ++a)
+      yf[ks][a] = lds_frag_xT<BM>(smem + J * C::Y_BYTES, ks * 16, wm * 128 + a * 32, lane);
+#pragma unroll
+    for (int b = 0; b < NI; ++b)
+      xf[ks][b] = frag_x<BN>(smem + C::X_AT + X * C::X_BYTES, ks * 16, wn * 64 + b * 32, lane);
+  };
+  // Two of a step's 16 matrix instructions; nothing is moved across.
+  auto multiply = [&](int ks, int a) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < NI; ++b)
+      acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf[ks][b], yf[ks][a], acc[a][b], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using std::false_type;
+  using std::integral_constant;
+  using std::true_type;
+  // The waves 0-3 and 4-7 (a wave of each on every SIMD) run half a step apart.
+  // Step k is a memory phase, in which a wave reads its fragments of the step
+  // and its x bytes of step k + 2, and a compute phase, in which it multiplies,
+  // issues the loads of dy for step k + 3 and of x for step k + 4 and writes its
+  // bf16 x of step k + 2.  A barrier closes each; the second group enters the
+  // loop one barrier late and the first leaves it one late, so while one group
+  // multiplies the other reads.  With phases numbered by barriers, the first
+  // group reads step k in phase 2k and writes in 2k + 1, the second in 2k + 1 and
+  // 2k + 2: x of step k + 2 is complete before phase 2k + 4 reads it, and its
+  // tile, as the dy buffer of step k + 3, was last read in phases 2k - 3 and
+  // 2k - 1.
+  auto step = [&](auto n, auto end, int k) {
+    constexpr int I = decltype(n)::value;
+    constexpr bool END = decltype(end)::value;
+    constexpr int SLOT = C::Q_AT + I % C::QS * C::QW_BYTES;
+    integral_constant<int, (I + 1) % C::YS> buf_1;
+    integral_constant<int, (I + 3) % C::YS> buf_3;
+    integral_constant<int, (I + 2) % C::XS> tile_2;
+    // dy of step k + 1 and x of step k + 2 are there: only what the last compute
+    // phase issued may be in flight
+    if (!END || k + 3 < steps)
+      wait_vmcnt<C::Y_INSTR + 2>();
+    else if (k + 2 < steps)
+      wait_vmcnt<C::Y_INSTR>();
+    else
+      wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+    const bool more_x = !END || k + 2 < steps, more_y = !END || k + 3 < steps,
+               more_q = !END || k + 4 < steps;
+    if (more_x) read_q(SLOT);
+    frags(n, n, 0);
+    frags(n, n, 1);
+    if (END && k + 2 == steps && last < BK) zero_tail(buf_1);
+    block_barrier();
+    multiply(0, 0);
+    if (more_y) issue_y(buf_3, end, 0, k + 3);
+    multiply(0, 1);
+    if (more_y) issue_y(buf_3, end, 1, k + 3);
+    multiply(0, 2);
+    if (more_q) issue_q(end, SLOT, k + 4);
+    multiply(0, 3);
+    if (more_q) issue_s(end, SLOT, k + 4);
+    multiply(1, 0);
+    if (more_x) unpack();
+    multiply(1, 1);
+    if (more_x) write_x(tile_2);
+    multiply(1, 2);
+    multiply(1, 3);
+    block_barrier();
+  };
+  if (steps > 0) {
+    static_assert(C::YS == 4 && C::XS == 4 && C::QS == 2, "the loop is unrolled by 4");
+    integral_constant<int, 0> c0;
+    integral_constant<int, 1> c1;
+    integral_constant<int, 2> c2;
+    integral_constant<int, 3> c3;
+    true_type end;
+    // the x bytes of steps 0 and 1 wait in the x tiles of steps 2 and 3
+    constexpr int Q0 = C::X_AT + 2 * C::X_BYTES, Q1 = C::X_AT + 3 * C::X_BYTES;
+    auto issue_x = [&](int at, int k) {
+      issue_q(end, at, k);
+      issue_s(end, at, k);
+    };
+    issue_x(Q0, 0);
+    if (1 < steps) issue_x(Q1, 1);
+    for (int i = 0; i < C::Y_INSTR; ++i) issue_y(c0, end, i, 0);
+    if (1 < steps)
+      for (int i = 0; i < C::Y_INSTR; ++i) issue_y(c1, end, i, 1);
+    if (2 < steps) {
+      issue_x(C::Q_AT, 2);
+      for (int i = 0; i < C::Y_INSTR; ++i) issue_y(c2, end, i, 2);
+    }
+    if (3 < steps) issue_x(C::Q_AT + C::QW_BYTES, 3);
+    // steps 0 and 1 of x, and step 0 of dy: all but the loads behind it
+    if (3 < steps)
+      wait_vmcnt<2 * C::Y_INSTR + 4>();
+    else if (2 < steps)
+      wait_vmcnt<2 * C::Y_INSTR + 2>();
+    else if (1 < steps)
+      wait_vmcnt<C::Y_INSTR>();
+    else
+      wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+    read_q(Q0);
+    unpack();
+    write_x(c0);
+    if (1 < steps) {
+      read_q(Q1);
+      unpack();
+      write_x(c1);
+    }
+    if (steps == 1 && last < BK) zero_tail(c0);
+    block_barrier();
+    if (wave >= 4) block_barrier();
+    int k = 0;
+    for (; k + 8 < steps; k += 4) {   // every load of a whole step
+      step(c0, false_type{}, k);
+      step(c1, false_type{}, k + 1);
+      step(c2, false_type{}, k + 2);
+      step(c3, false_type{}, k + 3);
+    }
+    for (; k < steps; k += 4) {
+      step(c0, end, k);
+      if (k + 1 < steps) step(c1, end, k + 1);
+      if (k + 2 < steps) step(c2, end, k + 2);
+      if (k + 3 < steps) step(c3, end, k + 3);
+    }
+    if (wave < 4) block_barrier();
+  }
+  if (pc.parts == 1 && steps == 0 && p.accumulate) return;
+  store_tile<MI>(p, pc, i0 + wm * 128, j0 + wn * 64, acc, smem + wave * kWindow, lane);
+}
+
+// Adds the partial sums of the matrices with several pieces, in their order:
+// kJoin elements at a time.
+constexpr int kJoin = 8 * kThreads;
+__global__ __launch_bounds__(kThreads) void join_kernel(const WeightGrad p, int64_t blocks) {
+  const int64_t size = int64_t(p.rows) * p.cols;
+  const Split* splits = reinterpret_cast<const Split*>(static_cast<const Piece*>(p.table) + p.pieces);
+  const int64_t work = p.offsets ? splits[p.count].e * blocks : blocks;
+  for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
+    const int64_t which = i / blocks, at = (i - which * blocks) * kJoin + threadIdx.x * 8;
+    const Split sp = p.offsets ? splits[which] : Split{0, int(p.pieces), 0};
+    if (at >= size) continue;
+    const int left = size - at < 8 ? int(size - at) : 8;
+    float v[8] = {};
+#pragma unroll 2
+    for (int j = 0; j < sp.parts; ++j) {
+      const float* part = p.partial + (sp.slot + j) * size + at;
+      float w[8];
+      load_vec<false>(part, 0, left, w);
+      load_vec<false>(part, 4, left, w + 4);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] += w[c];
+    }
+    // the matrix as one row
+    WeightGrad flat = p;
+    flat.rows = 1;
+    flat.cols = left;
+    store_row8(flat, nullptr, sp.e * size + at, 0, 0, f32x4_t{v[0], v[1], v[2], v[3]},
+               f32x4_t{v[4], v[5], v[6], v[7]});
+  }
 }
 
 int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
+
+// Parts that a matrix of `tokens` is cut into, `count` matrices at once: the
+// estimate below at its least.  In microseconds, measured on one MI355X: a
+// round of blocks (one per CU) takes 6 (start, first loads, stores) and 0.95
+// for each step of 32 tokens; the join takes 4 and, through the Infinity Cache,
+// moves 8 bytes per element and part at 10 TB/s.  4096 x 1024 over 16384 tokens, 64 tiles: 182 us in 2
+// parts, 131 in 4, 151 in 8.
+int64_t parts_of(int64_t count, int64_t tokens, int64_t rows, int64_t cols, int64_t tiles) {
+  const double steps = double(cdiv(tokens, BK)), g = double(count) * double(rows) * double(cols);
+  int64_t best = 1;
+  double least = 0;
+  for (int64_t n = 1; n <= 64 && n <= cdiv(tokens, 4 * BK); ++n) {
+    const double rounds = double(cdiv(count * tiles * n, 256));
+    const double us = rounds * (6 + 0.95 * steps / double(n)) + (n > 1 ? 4 + g * double(n) * 8 / 1e7 : 0);
+    if (n == 1 || us < least) {
+      best = n;
+      least = us;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
-// Pieces: enough blocks for two per CU, of at least 128 tokens each.
-WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int64_t cols) {
+// Ragged matrices are taken as even for the cut; the uneven ones get pieces
+// of at most that length or, where it is more, of an even share of the whole
+// call per CU (64 experts of 1408 x 512 over 49152 tokens, a spread of 3:1:
+// 134 us in pieces of 1024, 120 of 2048 to 4096, 123 of 8192).
+WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int64_t cols,
+                                bool ragged) {
   constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
   WeightGradPlan w{};
-  w.bm = BM;
-  w.bn = BN;
-  w.tiles = cdiv(rows, BM) * cdiv(cols, BN);
-  const int64_t want = std::max<int64_t>(count, 512 / w.tiles);
-  const int64_t chunk = std::max<int64_t>(128, cdiv(cdiv(tokens, want), BK) * BK);
+  const int64_t tiles = cdiv(rows, Wide::BM) * cdiv(cols, Wide::BN);
+  const int64_t even = cdiv(tokens, count);
+  int64_t chunk = cdiv(even, parts_of(count, even, rows, cols, tiles));
+  if (ragged) chunk = std::max(chunk, tokens / 256 * tiles);
+  chunk = std::max<int64_t>(4 * BK, cdiv(std::min(chunk, MUON_MAX_TOKENS), BK) * BK);
   w.chunk = uint32_t(chunk);
-  if (count == 1) {
+  if (!ragged) {
     w.pieces = std::max<int64_t>(1, cdiv(tokens, chunk));
     w.slots = w.pieces > 1 ? w.pieces : 0;
   } else {
+    // a matrix of n > 1 pieces has more than (n - 1) chunk tokens
     w.pieces = tokens / chunk + count;
-    w.slots = tokens > chunk ? std::min(2 * tokens / chunk, w.pieces) : 0;
+    w.slots = tokens > chunk ? std::min(2 * (tokens / chunk) + 1, w.pieces) : 0;
+    w.table_bytes = w.pieces * kWeightGradPieceBytes + (count + 1) * kWeightGradSplitBytes;
   }
-  if (w.pieces * w.tiles > kMaxBlocks || 4 * count * w.tiles > kMaxBlocks) {
+  // the largest grid: the smallest tiles, and whole turns of the 8 XCDs
+  if ((w.pieces + 64) * (cdiv(rows, BM) * cdiv(cols, BN)) > kMaxBlocks) {
     w.pieces = 0;
     return w;
   }
-  w.partial_bytes = size_t(w.slots) * size_t(w.tiles) * kTile * 4;
+  w.partial_bytes = size_t(w.slots) * size_t(rows) * size_t(cols) * 4;
   return w;
 }
 
 hipError_t launch_weight_grad(const WeightGrad& p, const WeightGradPlan& plan, bool bf16,
                               hipStream_t s) {
-  const int tiles_n = int(cdiv(p.cols, BN));
-  const dim3 grid(unsigned(plan.pieces * plan.tiles));
+  // The 256 x 256 tiles need 16-byte rows of dy, and enough work: below four
+  // steps per CU the 128 x 128 tiles, four times as many and quicker to start,
+  // are ahead (768 x 768: 7.4 against 10.3 us over 96 tokens, 15.4 against 18.4
+  // over 512, 42.2 against 33.9 over 8192).
+  const bool rows16 = p.rows % 8 == 0 && p.lddy % 8 == 0 && reinterpret_cast<uintptr_t>(p.dy) % 16 == 0;
+  const int64_t wide_steps = cdiv(p.tokens, BK) * cdiv(p.rows, Wide::BM) * cdiv(p.cols, Wide::BN);
+  // a multiple of 8 blocks; with offsets, whole turns of `deal` tiles per XCD
+  auto grid = [&](int tm, int tn) {
+    const int64_t tiles = int64_t(tm) * tn, deal = p.offsets ? std::min<int64_t>(tiles, 32) : 1;
+    return dim3(unsigned(cdiv(plan.pieces * tiles, 8 * deal) * 8 * deal));
+  };
+  if (p.offsets) {
+    if (p.count <= 64)
+      hipLaunchKernelGGL(plan_kernel<64>, dim3(1), dim3(64), 0, s, p);
+    else
+      hipLaunchKernelGGL(plan_kernel<kPlanThreads>, dim3(1), dim3(kPlanThreads), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (bf16 && rows16 && wide_steps >= 4 * 256) {
+    const int tm = int(cdiv(p.rows, Wide::BM)), tn = int(cdiv(p.cols, Wide::BN));
+    if (p.x.fmt == MUON_CKPT_E4M3)
+      hipLaunchKernelGGL((weight_grad_wide_kernel<MUON_CKPT_E4M3>), grid(tm, tn), dim3(64 * Wide::NW),
+                         0, s, p, tm, tn);
+    else
+      hipLaunchKernelGGL((weight_grad_wide_kernel<MUON_CKPT_INT8>), grid(tm, tn), dim3(64 * Wide::NW),
+                         0, s, p, tm, tn);
+    return hipGetLastError();
+  }
+  const int tm = int(cdiv(p.rows, BM)), tn = int(cdiv(p.cols, BN));
   if (bf16)
-    hipLaunchKernelGGL(weight_grad_kernel<true>, grid, dim3(NT), 0, s, p, tiles_n, int(plan.tiles));
+    hipLaunchKernelGGL(weight_grad_kernel<true>, grid(tm, tn), dim3(kThreads), 0, s, p, tm, tn);
   else
-    hipLaunchKernelGGL(weight_grad_kernel<false>, grid, dim3(NT), 0, s, p, tiles_n, int(plan.tiles));
+    hipLaunchKernelGGL(weight_grad_kernel<false>, grid(tm, tn), dim3(kThreads), 0, s, p, tm, tn);
   return hipGetLastError();
 }
 
 hipError_t launch_weight_grad_join(const WeightGrad& p, const WeightGradPlan& plan, hipStream_t s) {
-  const int tiles_n = int(cdiv(p.cols, BN));
-  hipLaunchKernelGGL(join_kernel, dim3(unsigned(4 * p.count * plan.tiles)), dim3(NT), 0, s, p,
-                     tiles_n, int(plan.tiles));
+  const int64_t blocks = cdiv(int64_t(p.rows) * p.cols, kJoin);
+  const int64_t most = p.offsets ? std::max<int64_t>(1, plan.slots / 2) : 1;   // split matrices
+  hipLaunchKernelGGL(join_kernel, dim3(unsigned(std::min<int64_t>(most * blocks, 4096))), dim3(kThreads), 0,
+                     s, p, blocks);
   return hipGetLastError();
 }
 

@@ -11,7 +11,6 @@ using namespace muon;
 namespace {
 
 constexpr size_t kAlign = 256;
-constexpr int64_t kMaxGrid = (int64_t(1) << 24) - 1;
 
 bool dtype_ok(int dtype) { return dtype == MUON_DTYPE_F32 || dtype == MUON_DTYPE_BF16; }
 size_t elem_size(int dtype) { return dtype == MUON_DTYPE_BF16 ? 2 : 4; }
@@ -94,6 +93,13 @@ int launched(hipError_t e, const char* what, hipStream_t s) {
   if (debug_sync_enabled())
     std::fprintf(stderr, "muon: %s failed: %s\n", what, hipGetErrorString(e));
   return MUON_ERR_HIP;
+}
+
+size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+
+// Workspace of a weight gradient (0: the sizes cannot be launched).
+size_t weight_grad_bytes(const WeightGradPlan& plan) {
+  return plan.pieces > 0 ? align_up(plan.partial_bytes) + align_up(plan.table_bytes) + kAlign : 0;
 }
 
 char* align_ptr(void* p) {
@@ -256,10 +262,9 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
 }
 
 size_t muon_weight_grad_workspace_bytes(int64_t count, int64_t tokens, int64_t rows, int64_t cols) {
-  if (count < 1 || count > kMaxGrid || !sizes_ok(tokens, cols) || rows < 1 || rows > MUON_MAX_DIM)
+  if (count < 1 || count > MUON_WEIGHT_GRAD_MAX_COUNT || !sizes_ok(tokens, cols) || rows < 1 || rows > MUON_MAX_DIM)
     return 0;
-  const WeightGradPlan plan = weight_grad_plan(count, tokens, rows, cols);
-  return plan.pieces > 0 ? plan.partial_bytes + kAlign : 0;
+  return weight_grad_bytes(weight_grad_plan(count, tokens, rows, cols, true));
 }
 
 int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x,
@@ -268,7 +273,7 @@ int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x
   if (!dtype_ok(dtype) || !dtype_ok(g_dtype)) return MUON_ERR_UNSUPPORTED_DTYPE;
   if (count < 0 || !x) return MUON_ERR_INVALID_ARGUMENT;
   const int64_t tokens = x->tokens, cols = x->cols;
-  if (rows < 1 || rows > MUON_MAX_DIM || count > kMaxGrid) return MUON_ERR_INVALID_SHAPE;
+  if (rows < 1 || rows > MUON_MAX_DIM || count > MUON_WEIGHT_GRAD_MAX_COUNT) return MUON_ERR_INVALID_SHAPE;
   if (const int st = check_ckpt(x, tokens, cols); st != MUON_OK) return st;
   if (count == 0) return MUON_OK;
   if (!offsets && count != 1) return MUON_ERR_INVALID_ARGUMENT;
@@ -286,9 +291,9 @@ int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x
   b.add(G, g_bytes, true);
   b.add(workspace, workspace_bytes, true);
   if (b.clash()) return MUON_ERR_INVALID_ARGUMENT;
-  const WeightGradPlan plan = weight_grad_plan(count, tokens, rows, cols);
+  const WeightGradPlan plan = weight_grad_plan(count, tokens, rows, cols, offsets != nullptr);
   if (plan.pieces <= 0) return MUON_ERR_INVALID_SHAPE;
-  if (workspace_bytes < plan.partial_bytes + kAlign) return MUON_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < weight_grad_bytes(plan)) return MUON_ERR_WORKSPACE_TOO_SMALL;
   if (tokens == 0 && accumulate) return MUON_OK;
   WeightGrad p{};
   p.dy = dy;
@@ -305,6 +310,7 @@ int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x
   p.partial = reinterpret_cast<float*>(align_ptr(workspace));
   p.chunk = plan.chunk;
   p.pieces = plan.pieces;
+  p.table = reinterpret_cast<char*>(p.partial) + align_up(plan.partial_bytes);
   Trace t("muon_weight_grad");
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int st = launched(launch_weight_grad(p, plan, dtype == MUON_DTYPE_BF16, s), "weight_grad", s);

@@ -281,20 +281,23 @@ struct WeightGrad {
   int count, rows, cols;
   void* G;
   int g_bf16, accumulate;
-  float* partial;          // [slot][tile][tile elements]
+  float* partial;          // [slot][rows][cols]
   // A matrix's tokens are cut into pieces of `chunk`; a matrix of more than
   // one piece leaves partial sums in consecutive slots.
   uint32_t chunk;
   int64_t pieces;          // upper bound over all matrices
+  void* table;             // with offsets: the pieces and the split matrices
 };
-// The tile and the cut that the launchers use; also sizes the workspace.
+// The cut of the tokens, which also sizes the workspace: partial sums, then
+// (ragged) the table.
+constexpr int kWeightGradPieceBytes = 32, kWeightGradSplitBytes = 16;
 struct WeightGradPlan {
-  int bm, bn;
   uint32_t chunk;
-  int64_t pieces, slots, tiles;
-  size_t partial_bytes;
+  int64_t pieces, slots;
+  size_t partial_bytes, table_bytes;
 };
-WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int64_t cols);
+WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int64_t cols,
+                                bool ragged);
 hipError_t launch_weight_grad(const WeightGrad& p, const WeightGradPlan& plan, bool bf16,
                               hipStream_t s);
 hipError_t launch_weight_grad_join(const WeightGrad& p, const WeightGradPlan& plan, hipStream_t s);

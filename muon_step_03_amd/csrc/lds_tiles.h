@@ -50,6 +50,13 @@ __device__ __forceinline__ void dma16(uint32_t off, const char* base, uint32_t l
                : "v"(off), "s"(base), "s"(lds_base)
                : "memory", "m0");
 }
+// The same for 4 bytes per lane.
+__device__ __forceinline__ void dma4(uint32_t off, const char* base, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds_base)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
 
 // Workgroup barrier that publishes this wave's LDS traffic (lgkmcnt(0): its
