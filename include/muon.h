@@ -365,7 +365,8 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
  * parts, which hold its 24 bits) and accumulate in float32; G is rounded once.
  */
 #define MUON_WEIGHT_GRAD_MAX_COUNT (1 << 20)
-size_t muon_weight_grad_workspace_bytes(int64_t count, int64_t tokens, int64_t rows, int64_t cols);
+size_t muon_weight_grad_workspace_bytes(int64_t count, int64_t tokens, int64_t rows, int64_t cols,
+                                        int dtype);
 int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x,
                      const int64_t* offsets, int64_t count, int64_t rows, void* G, int g_dtype,
                      int accumulate, void* workspace, size_t workspace_bytes, void* stream);

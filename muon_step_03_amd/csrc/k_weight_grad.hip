@@ -474,7 +474,9 @@ __device__ __forceinline__ void unpack16(u32x4_t q, int byte, uint32_t (&o)[8]) 
   }
 }
 
-template <int FMT>
+// PARTS == 3: dy in three bf16 parts, a matrix of all tokens each (float32 dy);
+// the parts of 32 tokens are three steps in a row.
+template <int PARTS, int FMT>
 __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
     const WeightGrad p, int tiles_m, int tiles_n) {
   using C = Wide;
@@ -492,22 +494,22 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / C::WGN, wn = wave % C::WGN;
   const int len = pc.end - pc.begin;
-  const int steps = (len + BK - 1) / BK;
-  const int last = len - (steps - 1) * BK;   // tokens of the last step
+  const int blocks = (len + BK - 1) / BK, steps = blocks * PARTS;
+  const int last = len - (blocks - 1) * BK;   // tokens of the last block
 
   // Addresses of this lane's loads within a step.  Columns past a row's end
   // read its last ones instead (they only reach elements of G that are not
   // stored), tokens past the end the last token (their dy is zeroed below).
   int y_k[C::Y_INSTR];
   uint32_t y_off[C::Y_INSTR];
-  const uint32_t y_ld = uint32_t(p.lddy) * 2;
+  const uint32_t y_ld = uint32_t(p.y_ld) * 2;
 #pragma unroll
   for (int i = 0; i < C::Y_INSTR; ++i) {
     constexpr int CPR = BM / 8;   // chunks per token row
     const int at = (wave * C::Y_INSTR + i) * 64 + lane;
     y_k[i] = at / CPR;
     const int col = i0 + ((at % CPR) ^ gswz(y_k[i])) * 8;
-    y_off[i] = uint32_t(y_k[i]) * y_ld + uint32_t(col < p.rows ? col : p.rows - 8) * 2;
+    y_off[i] = uint32_t(y_k[i]) * y_ld + uint32_t(col < p.y_cols ? col : p.y_cols - 8) * 2;
   }
   constexpr int XL = BN / 16;     // lanes per token row of x
   const int x_k = wave * (64 / XL) + lane / XL, x_c = lane % XL;
@@ -515,29 +517,31 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
   const uint32_t q_ld = uint32_t(p.x.q_pitch), s_ld = uint32_t(p.x.s_pitch);
   const uint32_t q_off = uint32_t(x_k) * q_ld + (x_col < int(q_ld) ? x_col : int(q_ld) - 16);
   const uint32_t s_off = uint32_t(x_k) * s_ld + (s_col < int(s_ld) ? s_col : int(s_ld) - 4);
-  const char* y_base = static_cast<const char*>(p.dy) + int64_t(pc.begin) * y_ld;
+  const char* y_base = reinterpret_cast<const char*>(p.y) + int64_t(pc.begin) * y_ld;
   const char* q_base = reinterpret_cast<const char*>(p.x.q) + int64_t(pc.begin) * q_ld;
   const char* s_base = reinterpret_cast<const char*>(p.x.scale) + int64_t(pc.begin) * s_ld;
 
+  auto block_of = [](int k) { return PARTS == 1 ? k : int(uint32_t(k) / PARTS); };
   // Loads of step k: dy into buffer J; the bytes and scales of x to byte `at` of
-  // LDS.  END: k may be the last step.
+  // LDS.  END: k may be of
+  // the last tokens.
   auto issue_y = [&](auto buf, auto end, int i, int k) {
     constexpr int J = decltype(buf)::value;
     uint32_t off = y_off[i];
-    if (decltype(end)::value && k == steps - 1 && y_k[i] >= last)
+    if (decltype(end)::value && k >= steps - PARTS && y_k[i] >= last)
       off -= uint32_t(y_k[i] - (last - 1)) * y_ld;
-    dma16(off, y_base + int64_t(k) * BK * y_ld,
+    dma16(off, y_base + int64_t(block_of(k)) * BK * y_ld + int64_t(k - block_of(k) * PARTS) * p.y_part,
           smem_base + J * C::Y_BYTES + (wave * C::Y_INSTR + i) * WAVE_BYTES);
   };
   auto issue_q = [&](auto end, int at, int k) {
     uint32_t off = q_off;
-    if (decltype(end)::value && k == steps - 1 && x_k >= last) off -= uint32_t(x_k - (last - 1)) * q_ld;
-    dma16(off, q_base + int64_t(k) * BK * q_ld, smem_base + at + wave * WAVE_BYTES);
+    if (decltype(end)::value && k >= steps - PARTS && x_k >= last) off -= uint32_t(x_k - (last - 1)) * q_ld;
+    dma16(off, q_base + int64_t(block_of(k)) * BK * q_ld, smem_base + at + wave * WAVE_BYTES);
   };
   auto issue_s = [&](auto end, int at, int k) {
     uint32_t off = s_off;
-    if (decltype(end)::value && k == steps - 1 && x_k >= last) off -= uint32_t(x_k - (last - 1)) * s_ld;
-    dma4(off, s_base + int64_t(k) * BK * s_ld, smem_base + at + C::Q_BYTES + wave * 256);
+    if (decltype(end)::value && k >= steps - PARTS && x_k >= last) off -= uint32_t(x_k - (last - 1)) * s_ld;
+    dma4(off, s_base + int64_t(block_of(k)) * BK * s_ld, smem_base + at + C::Q_BYTES + wave * 256);
   };
   // This wave's x bytes of a step, and its part of their bf16 tile X.
   u32x4_t q;
@@ -624,7 +628,7 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
     if (more_x) read_q(SLOT);
     frags(n, n, 0);
     frags(n, n, 1);
-    if (END && k + 2 == steps && last < BK) zero_tail(buf_1);
+    if (END && k + 1 < steps && k + 1 >= steps - PARTS && last < BK) zero_tail(buf_1);
     block_barrier();
     multiply(0, 0);
     if (more_y) issue_y(buf_3, end, 0, k + 3);
@@ -683,11 +687,11 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
       unpack();
       write_x(c1);
     }
-    if (steps == 1 && last < BK) zero_tail(c0);
+    if (steps <= PARTS && last < BK) zero_tail(c0);
     block_barrier();
     if (wave >= 4) block_barrier();
     int k = 0;
-    for (; k + 8 < steps; k += 4) {   // every load of a whole step
+    for (; k + 7 + PARTS < steps; k += 4) {   // every load of whole steps
       step(c0, false_type{}, k);
       step(c1, false_type{}, k + 1);
       step(c2, false_type{}, k + 2);
@@ -703,6 +707,43 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
   }
   if (pc.parts == 1 && steps == 0 && p.accumulate) return;
   store_tile<MI>(p, pc, i0 + wm * 128, j0 + wn * 64, acc, smem + wave * kWindow, lane);
+}
+
+// dy as the wide tiles read it: bf16 rows padded with zeros to whole 16-byte
+// vectors; float32 in three parts of 8 bits each (truncation, remainders
+// exact; an infinity leaves no remainder).
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void repack_kernel(const void* dy, int64_t lddy,
+                                                          int64_t tokens, int rows, uint16_t* out,
+                                                          int64_t out_ld, int64_t out_part) {
+  using T = typename RowVec<BF16>::T;
+  constexpr int N = RowVec<BF16>::N, P = BF16 ? 1 : 3;
+  const uint32_t vecs = uint32_t(out_ld / 8);
+  const int64_t total = tokens * vecs;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += int64_t(gridDim.x) * kThreads) {
+    const int64_t t = i / vecs;
+    const int col = int(i - t * vecs) * 8;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += N) load_vec<BF16>(static_cast<const T*>(dy) + t * lddy, col + j, rows, v + j);
+#pragma unroll
+    for (int part = P - 1; part >= 0; --part) {   // the smallest part first in memory
+      u32x4_t w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = __float_as_uint(v[2 * j]) & 0xffff0000u;
+        const uint32_t b = __float_as_uint(v[2 * j + 1]) & 0xffff0000u;
+        w[j] = (a >> 16) | b;
+        if (part > 0) {
+          const float fa = __uint_as_float(a), fb = __uint_as_float(b);
+          v[2 * j] = v[2 * j] == fa ? 0.f : v[2 * j] - fa;
+          v[2 * j + 1] = v[2 * j + 1] == fb ? 0.f : v[2 * j + 1] - fb;
+        }
+      }
+      *reinterpret_cast<u32x4_t*>(out + part * out_part + t * out_ld + col) = w;
+    }
+  }
 }
 
 // Adds the partial sums of the matrices with several pieces, in their order:
@@ -767,10 +808,18 @@ int64_t parts_of(int64_t count, int64_t tokens, int64_t rows, int64_t cols, int6
 // call per CU (64 experts of 1408 x 512 over 49152 tokens, a spread of 3:1:
 // 134 us in pieces of 1024, 120 of 2048 to 4096, 123 of 8192).
 WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int64_t cols,
-                                bool ragged) {
+                                bool ragged, bool bf16) {
   constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
   WeightGradPlan w{};
   const int64_t tiles = cdiv(rows, Wide::BM) * cdiv(cols, Wide::BN);
+  // The 256 x 256 tiles need enough work: below four steps per CU the
+  // 128 x 128 tiles, four times as many and quicker to start, are ahead
+  // (768 x 768: 7.4 against 10.3 us over 96 tokens, 15.4 against 18.4 over 512,
+  // 42.2 against 33.9 over 8192).  They read 16-byte rows of bf16: float32 dy
+  // and rows of other lengths are repacked first.
+  w.wide = cdiv(tokens, BK) * tiles * (bf16 ? 1 : 3) >= 4 * 256;
+  if (w.wide && !(bf16 && rows % 8 == 0))
+    w.repack_bytes = size_t(tokens) * size_t(cdiv(rows, 8) * 8) * (bf16 ? 2 : 6);
   const int64_t even = cdiv(tokens, count);
   int64_t chunk = cdiv(even, parts_of(count, even, rows, cols, tiles));
   if (ragged) chunk = std::max(chunk, tokens / 256 * tiles);
@@ -794,14 +843,20 @@ WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int
   return w;
 }
 
-hipError_t launch_weight_grad(const WeightGrad& p, const WeightGradPlan& plan, bool bf16,
+template <int PARTS>
+hipError_t launch_wide(const WeightGrad& p, dim3 grid, int tm, int tn, hipStream_t s) {
+  if (p.x.fmt == MUON_CKPT_E4M3)
+    hipLaunchKernelGGL((weight_grad_wide_kernel<PARTS, MUON_CKPT_E4M3>), grid, dim3(64 * Wide::NW), 0,
+                       s, p, tm, tn);
+  else
+    hipLaunchKernelGGL((weight_grad_wide_kernel<PARTS, MUON_CKPT_INT8>), grid, dim3(64 * Wide::NW), 0,
+                       s, p, tm, tn);
+  return hipGetLastError();
+}
+
+hipError_t launch_weight_grad(const WeightGrad& call, const WeightGradPlan& plan, bool bf16,
                               hipStream_t s) {
-  // The 256 x 256 tiles need 16-byte rows of dy, and enough work: below four
-  // steps per CU the 128 x 128 tiles, four times as many and quicker to start,
-  // are ahead (768 x 768: 7.4 against 10.3 us over 96 tokens, 15.4 against 18.4
-  // over 512, 42.2 against 33.9 over 8192).
-  const bool rows16 = p.rows % 8 == 0 && p.lddy % 8 == 0 && reinterpret_cast<uintptr_t>(p.dy) % 16 == 0;
-  const int64_t wide_steps = cdiv(p.tokens, BK) * cdiv(p.rows, Wide::BM) * cdiv(p.cols, Wide::BN);
+  WeightGrad p = call;
   // a multiple of 8 blocks; with offsets, whole turns of `deal` tiles per XCD
   auto grid = [&](int tm, int tn) {
     const int64_t tiles = int64_t(tm) * tn, deal = p.offsets ? std::min<int64_t>(tiles, 32) : 1;
@@ -815,15 +870,28 @@ hipError_t launch_weight_grad(const WeightGrad& p, const WeightGradPlan& plan, b
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (bf16 && rows16 && wide_steps >= 4 * 256) {
+  const bool rows16 = p.rows % 8 == 0 && p.lddy % 8 == 0 && reinterpret_cast<uintptr_t>(p.dy) % 16 == 0;
+  if (plan.wide && (plan.repack_bytes > 0 || rows16)) {
+    p.y = static_cast<const uint16_t*>(p.dy);
+    p.y_ld = p.lddy;
+    p.y_cols = p.rows;
+    if (plan.repack_bytes > 0 && !(bf16 && rows16)) {
+      p.y = p.repack;
+      p.y_ld = p.y_cols = int(cdiv(p.rows, 8) * 8);
+      p.y_part = p.tokens * p.y_ld * 2;
+      const int64_t blocks = cdiv(p.tokens * (p.y_ld / 8), kThreads);
+      const dim3 g(unsigned(std::min<int64_t>(blocks, 16384)));
+      if (bf16)
+        hipLaunchKernelGGL(repack_kernel<true>, g, dim3(kThreads), 0, s, p.dy, p.lddy, p.tokens,
+                           p.rows, p.repack, p.y_ld, p.y_part / 2);
+      else
+        hipLaunchKernelGGL(repack_kernel<false>, g, dim3(kThreads), 0, s, p.dy, p.lddy, p.tokens,
+                           p.rows, p.repack, p.y_ld, p.y_part / 2);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
     const int tm = int(cdiv(p.rows, Wide::BM)), tn = int(cdiv(p.cols, Wide::BN));
-    if (p.x.fmt == MUON_CKPT_E4M3)
-      hipLaunchKernelGGL((weight_grad_wide_kernel<MUON_CKPT_E4M3>), grid(tm, tn), dim3(64 * Wide::NW),
-                         0, s, p, tm, tn);
-    else
-      hipLaunchKernelGGL((weight_grad_wide_kernel<MUON_CKPT_INT8>), grid(tm, tn), dim3(64 * Wide::NW),
-                         0, s, p, tm, tn);
-    return hipGetLastError();
+    return bf16 ? launch_wide<1>(p, grid(tm, tn), tm, tn, s) : launch_wide<3>(p, grid(tm, tn), tm, tn, s);
   }
   const int tm = int(cdiv(p.rows, BM)), tn = int(cdiv(p.cols, BN));
   if (bf16)

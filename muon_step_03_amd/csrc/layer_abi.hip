@@ -99,7 +99,9 @@ size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
 // Workspace of a weight gradient (0: the sizes cannot be launched).
 size_t weight_grad_bytes(const WeightGradPlan& plan) {
-  return plan.pieces > 0 ? align_up(plan.partial_bytes) + align_up(plan.table_bytes) + kAlign : 0;
+  return plan.pieces > 0 ? align_up(plan.partial_bytes) + align_up(plan.table_bytes) +
+                               plan.repack_bytes + kAlign
+                         : 0;
 }
 
 char* align_ptr(void* p) {
@@ -261,10 +263,12 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
   return launched(launch_ln_params(p, s), "layernorm_params", s);
 }
 
-size_t muon_weight_grad_workspace_bytes(int64_t count, int64_t tokens, int64_t rows, int64_t cols) {
-  if (count < 1 || count > MUON_WEIGHT_GRAD_MAX_COUNT || !sizes_ok(tokens, cols) || rows < 1 || rows > MUON_MAX_DIM)
+size_t muon_weight_grad_workspace_bytes(int64_t count, int64_t tokens, int64_t rows, int64_t cols,
+                                        int dtype) {
+  if (!dtype_ok(dtype) || count < 1 || count > MUON_WEIGHT_GRAD_MAX_COUNT || !sizes_ok(tokens, cols) || rows < 1 || rows > MUON_MAX_DIM)
     return 0;
-  return weight_grad_bytes(weight_grad_plan(count, tokens, rows, cols, true));
+  return weight_grad_bytes(
+      weight_grad_plan(count, tokens, rows, cols, true, dtype == MUON_DTYPE_BF16));
 }
 
 int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x,
@@ -291,7 +295,8 @@ int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x
   b.add(G, g_bytes, true);
   b.add(workspace, workspace_bytes, true);
   if (b.clash()) return MUON_ERR_INVALID_ARGUMENT;
-  const WeightGradPlan plan = weight_grad_plan(count, tokens, rows, cols, offsets != nullptr);
+  const WeightGradPlan plan = weight_grad_plan(count, tokens, rows, cols, offsets != nullptr,
+                                               dtype == MUON_DTYPE_BF16);
   if (plan.pieces <= 0) return MUON_ERR_INVALID_SHAPE;
   if (workspace_bytes < weight_grad_bytes(plan)) return MUON_ERR_WORKSPACE_TOO_SMALL;
   if (tokens == 0 && accumulate) return MUON_OK;
@@ -311,6 +316,7 @@ int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x
   p.chunk = plan.chunk;
   p.pieces = plan.pieces;
   p.table = reinterpret_cast<char*>(p.partial) + align_up(plan.partial_bytes);
+  p.repack = reinterpret_cast<uint16_t*>(static_cast<char*>(p.table) + align_up(plan.table_bytes));
   Trace t("muon_weight_grad");
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int st = launched(launch_weight_grad(p, plan, dtype == MUON_DTYPE_BF16, s), "weight_grad", s);

@@ -287,17 +287,24 @@ struct WeightGrad {
   uint32_t chunk;
   int64_t pieces;          // upper bound over all matrices
   void* table;             // with offsets: the pieces and the split matrices
+  uint16_t* repack;        // workspace for dy in aligned bf16 rows
+  // dy as the 256 x 256 tiles read it
+  const uint16_t* y;
+  int64_t y_ld;            // elements
+  int64_t y_part;          // bytes between the parts of float32 dy
+  int y_cols;              // columns that may be read
 };
 // The cut of the tokens, which also sizes the workspace: partial sums, then
-// (ragged) the table.
+// (ragged) the table, then dy repacked.
 constexpr int kWeightGradPieceBytes = 32, kWeightGradSplitBytes = 16;
 struct WeightGradPlan {
   uint32_t chunk;
   int64_t pieces, slots;
-  size_t partial_bytes, table_bytes;
+  bool wide;               // 256 x 256 tiles, where dy's rows allow
+  size_t partial_bytes, table_bytes, repack_bytes;
 };
 WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int64_t cols,
-                                bool ragged);
+                                bool ragged, bool bf16);
 hipError_t launch_weight_grad(const WeightGrad& p, const WeightGradPlan& plan, bool bf16,
                               hipStream_t s);
 hipError_t launch_weight_grad_join(const WeightGrad& p, const WeightGradPlan& plan, hipStream_t s);

@@ -282,8 +282,10 @@ def layernorm_backward(dy, x, gain, mean, rstd, *, bias=True, dgain=None, dbias=
     return dx, dgain, dbias
 
 
-def weight_grad_workspace_bytes(count: int, tokens: int, rows: int, cols: int) -> int:
-    return int(_lib.lib().muon_weight_grad_workspace_bytes(count, tokens, rows, cols))
+def weight_grad_workspace_bytes(count: int, tokens: int, rows: int, cols: int,
+                                dtype: torch.dtype) -> int:
+    return int(_lib.lib().muon_weight_grad_workspace_bytes(count, tokens, rows, cols,
+                                                           dtype_code(dtype)))
 
 
 def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, workspace=None,
@@ -330,7 +332,8 @@ def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, w
             G = torch.empty(shape, dtype=dtype or dy.dtype, device=dev)
         if count == 0:
             return G
-        ws = _workspace(weight_grad_workspace_bytes(count, tokens, rows, ck.cols), dev, workspace)
+        ws = _workspace(weight_grad_workspace_bytes(count, tokens, rows, ck.cols, dy.dtype), dev,
+                        workspace)
         st = _lib.lib().muon_weight_grad(
             dy.data_ptr(), ld, dt, _ref(ck), _ptr(offsets), count, rows, G.data_ptr(), gdt,
             int(accumulate), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev))

@@ -164,17 +164,22 @@ def test_workspace_sizes(L):
     # partial sums grow with the tokens up to a fixed number of blocks
     big = L.muon_layernorm_workspace_bytes(1 << 20, 1024)
     assert big == L.muon_layernorm_workspace_bytes(1 << 30, 1024) > 1024 * 8
-    assert L.muon_weight_grad_workspace_bytes(0, 5, 5, 5) == 0
-    assert L.muon_weight_grad_workspace_bytes(1, 5, 0, 5) == 0
-    assert L.muon_weight_grad_workspace_bytes(1, -1, 5, 5) == 0
-    assert L.muon_weight_grad_workspace_bytes(1, 5, 5, _lib.MUON_MAX_DIM + 1) == 0
-    assert L.muon_weight_grad_workspace_bytes(1, 0, 5, 5) >= 256
-    # partial sums: never more than a tile-padded G per 64 tokens and matrix
+    assert L.muon_weight_grad_workspace_bytes(0, 5, 5, 5, 0) == 0
+    assert L.muon_weight_grad_workspace_bytes(1, 5, 0, 5, 0) == 0
+    assert L.muon_weight_grad_workspace_bytes(1, -1, 5, 5, 0) == 0
+    assert L.muon_weight_grad_workspace_bytes(1, 5, 5, _lib.MUON_MAX_DIM + 1, 0) == 0
+    assert L.muon_weight_grad_workspace_bytes(1, 0, 5, 5, 0) >= 256
+    assert L.muon_weight_grad_workspace_bytes(1, 5, 5, 5, 2) == 0
+    # partial sums and a table entry for each piece of at least 128 tokens,
+    # and dy once more in three bf16 parts (float32) or in padded rows
     for count, tokens, rows, cols in [(1, 1 << 20, 64, 64), (64, 49152, 1408, 512),
-                                      (1, 16384, 4096, 1024), (7, 100, 33, 1000)]:
-        got = L.muon_weight_grad_workspace_bytes(count, tokens, rows, cols)
-        pad = (rows + 255) // 256 * 256 * ((cols + 255) // 256 * 256) * 4
-        assert 256 <= got <= 256 + pad * (tokens // 32 + count)
+                                      (1, 16384, 4096, 1024), (7, 100, 33, 1000),
+                                      (1, 65536, 1001, 777)]:
+        for dtype, part in ((F32, 6), (BF16, 0 if rows % 8 == 0 else 2)):
+            got = L.muon_weight_grad_workspace_bytes(count, tokens, rows, cols, dtype)
+            pieces = tokens // 128 + count
+            most = pieces * (rows * cols * 4 + 48) + (rows + 7) * tokens * part + 1024
+            assert 256 <= got <= most
 
 
 def test_binding_refuses_what_is_not_on_a_gpu():

@@ -208,6 +208,98 @@ def test_weight_grad_ragged(counts, dtype, fmt):
     check_weight(into, dy, x64, off.tolist(), before)
 
 
+# Sizes whose work takes the 256 x 256 tiles: whole and odd rows (repacked),
+# columns that end inside a tile, steps of 32 tokens that do not come out even.
+WIDE = [(4100, 1001, 1030), (8201, 520, 264), (33000, 256, 8), (2817, 1408, 512), (32800, 8, 100)]
+
+
+@pytest.mark.parametrize("tokens,rows,cols", WIDE)
+@pytest.mark.parametrize("dtype,gdtype,fmt", [(BF16, BF16, "int8"), (BF16, F32, "e4m3"),
+                                              (F32, F32, "int8"), (F32, BF16, "e4m3")])
+def test_weight_grad_wide(tokens, rows, cols, dtype, gdtype, fmt):
+    dy, ck, x64 = weight_case(tokens, rows, cols, dtype, fmt, seed=rows)
+    check_weight(M.weight_grad(dy, ck, dtype=gdtype), dy, x64)
+
+
+@pytest.mark.parametrize("counts", [
+    [0, 1, 31, 32, 33, 2000, 64, 0, 3839], [7000], [0, 6500, 0], [96] * 70, [3001, 3001],
+    [1] * 900 + [6200] + [0] * 300])
+@pytest.mark.parametrize("dtype,rows,fmt", [(BF16, 512, "e4m3"), (BF16, 517, "int8"), (F32, 512, "int8")])
+def test_weight_grad_wide_ragged(counts, dtype, rows, fmt):
+    cols = 520
+    if len(counts) > 64:
+        rows, cols = (rows + 7) // 8, 72      # many small matrices
+    tokens = sum(counts) + 3
+    dy, ck, x64 = weight_case(tokens, rows, cols, dtype, fmt, seed=len(counts))
+    off = offsets_of(counts)
+    before = torch.randn(len(counts), rows, cols, generator=torch.Generator().manual_seed(1))
+    before = before.to(dtype).to(DEV) * 1e-2
+    into = before.clone()
+    M.weight_grad(dy, ck, offsets=off.to(DEV), G=into, accumulate=True)
+    check_weight(into, dy, x64, off.tolist(), before)
+    check_weight(M.weight_grad(dy, ck, offsets=off.to(DEV)), dy, x64, off.tolist())
+
+
+@pytest.mark.parametrize("bad,read_as", [
+    ([-50, 3000, 9000, 10 ** 12], [0, 3000, 8000, 8000]),
+    ([0, 8000, 0, 8000, 0, 8000], [0, 8000, 8000, 8000, 8000, 8000]),
+])
+def test_weight_grad_wide_bad_offsets(bad, read_as):
+    dy, ck, x64 = weight_case(8000, 512, 260, BF16, "int8")
+    G = M.weight_grad(dy, ck, offsets=torch.tensor(bad, dtype=torch.int64, device=DEV))
+    check_weight(G, dy, x64, read_as)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens,rows,cols", [(8192, 512, 512), (5003, 700, 300), (5003, 701, 300)])
+def test_weight_grad_wide_exact_integers(dtype, tokens, rows, cols):
+    g = torch.Generator().manual_seed(tokens + rows)
+    x = torch.randint(-1, 2, (tokens, cols), generator=g).float()
+    lim = 128 if dtype == BF16 else 1900
+    dy = torch.randint(-lim, lim + 1, (tokens, rows), generator=g).float()
+    want = dy.double().t() @ x.double()
+    assert float(want.abs().max()) < 2 ** 24
+    dy = dy.to(dtype).to(DEV)
+    for fmt in FMTS:
+        ck = M.checkpoint_save(x.to(dtype).to(DEV), fmt)
+        assert torch.equal(M.weight_grad(dy, ck, dtype=F32).cpu().double(), want)
+    # a strided view: its own row stride, 16-byte rows or (from an odd column) not
+    wide = torch.full((tokens, rows + 24), float("nan"), dtype=dtype, device=DEV)
+    for start in (8, 3):
+        view = wide[:, start:start + rows]
+        view.copy_(dy)
+        assert torch.equal(M.weight_grad(view, ck, dtype=F32).cpu().double(), want)
+        wide.fill_(float("nan"))
+
+
+@pytest.mark.parametrize("dtype,rows", [(BF16, 512), (BF16, 500), (BF16, 501), (F32, 256)])
+def test_weight_grad_wide_keeps_bad_tokens_apart(dtype, rows):
+    """NaN and infinities of one matrix's tokens, and of its neighbours' in the
+    same steps, stay out of the others."""
+    tokens, cols = 9000, 512
+    dy, x = grads(tokens, rows, dtype, seed=6), hidden(tokens, cols, dtype, seed=6)
+    off = torch.tensor([0, 3001, 3002, 9000], dtype=torch.int64, device=DEV)
+    clean = M.weight_grad(dy, M.checkpoint_save(x, "int8"), offsets=off)
+    dy[3001, :] = float("nan")
+    x[3001, 40] = float("inf")
+    for fmt in FMTS:
+        ck = M.checkpoint_save(x, fmt)
+        got = M.weight_grad(dy, ck, offsets=off)
+        assert bool(got[1].isnan().all()) and not bool(got[[0, 2]].isnan().any())
+        if fmt == "int8":
+            assert torch.equal(got[0], clean[0]) and torch.equal(got[2], clean[2])
+    dy[3001, :] = 1.0
+    dy[3001, 5] = float("inf")
+    x[3001, 40] = 2.0
+    x[3001, 64:96] = float("inf")      # a marked block
+    x[3001, 96:128] = 3.0
+    for fmt in FMTS:
+        got = M.weight_grad(dy, M.checkpoint_save(x, fmt), offsets=off)
+        assert bool(got[1][:, 64:96].isnan().all()) and not bool(got[[0, 2]].isnan().any())
+        assert bool((got[1][5, 96:128] == float("inf")).all())
+        assert bool(got[1][torch.arange(rows) != 5][:, 96:128].isfinite().all())
+
+
 def test_weight_grad_offsets_start_late():
     dy, ck, x64 = weight_case(300, 64, 64, BF16, "e4m3")
     off = torch.tensor([17, 100, 100, 260], dtype=torch.int64)
@@ -282,7 +374,7 @@ def test_same_bits_every_time_and_given_buffers():
     first = M.layernorm_backward(dy, x, gain, out.mean, out.rstd)
     G = M.weight_grad(dy, out.y_checkpoint)
     ws = torch.full((max(M.layernorm_workspace_bytes(3000, 520),
-                         M.weight_grad_workspace_bytes(1, 3000, 520, 520)),), 255,
+                         M.weight_grad_workspace_bytes(1, 3000, 520, 520, BF16)),), 255,
                     dtype=torch.uint8, device=DEV)
     for _ in range(3):
         again = M.layernorm_backward(dy, x, gain, out.mean, out.rstd, workspace=ws)
