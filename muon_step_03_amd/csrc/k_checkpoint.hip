@@ -29,7 +29,7 @@ __global__ __launch_bounds__(kThreads) void save_kernel(const void* x, int64_t l
        base += int64_t(gridDim.x) * (kThreads * kPerThread)) {
     const int64_t row0 = base / vpr;
     const uint32_t rem = uint32_t(base - row0 * vpr);
-    float v[kPerThread][N];
+    u32x4_t w[kPerThread];
     int64_t row[kPerThread];
     int col[kPerThread];
 #pragma unroll
@@ -38,18 +38,15 @@ __global__ __launch_bounds__(kThreads) void save_kernel(const void* x, int64_t l
       const uint32_t r = at / vpr;
       row[j] = row0 + r;
       col[j] = int((at - r * vpr) * N);
-      if (row[j] < tokens) {
-        load_vec<BF16>(static_cast<const typename R::T*>(x) + row[j] * ldx, col[j], cols, v[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[j][i] = 0.f;
-      }
+      w[j] = u32x4_t{0, 0, 0, 0};
+      if (row[j] < tokens)
+        w[j] = load_raw<BF16>(static_cast<const typename R::T*>(x) + row[j] * ldx, col[j], cols);
     }
     // blocks of a row never straddle a wave (vpr is a multiple of 16), and the
     // lanes of one block lie in one row: they all pass the test below together
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j)
-      if (row[j] < tokens) ckpt_store<N>(c, row[j], col[j], cols, v[j]);
+      if (row[j] < tokens) ckpt_store<BF16>(c, row[j], col[j], cols, w[j]);
   }
 }
 
@@ -64,7 +61,7 @@ __global__ __launch_bounds__(kThreads) void restore_kernel(Ckpt c, void* x, int6
        base += int64_t(gridDim.x) * (kThreads * kPerThread)) {
     const int64_t row0 = base / vpr;
     const uint32_t rem = uint32_t(base - row0 * vpr);
-    float v[kPerThread][N];
+    CkptVec<N> r8[kPerThread];
     int64_t row[kPerThread];
     int col[kPerThread];
 #pragma unroll
@@ -73,12 +70,15 @@ __global__ __launch_bounds__(kThreads) void restore_kernel(Ckpt c, void* x, int6
       const uint32_t r = at / vpr;
       row[j] = row0 + r;
       col[j] = int((at - r * vpr) * N);
-      if (row[j] < tokens) ckpt_load<N>(c, row[j], col[j], v[j]);
+      if (row[j] < tokens) r8[j] = ckpt_load<N>(c, row[j], col[j]);
     }
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j)
-      if (row[j] < tokens)
-        store_vec<BF16>(static_cast<typename R::T*>(x) + row[j] * cols, col[j], cols, v[j]);
+      if (row[j] < tokens) {
+        float v[N];
+        ckpt_values<N>(r8[j], c.fmt, v);
+        store_vec<BF16>(static_cast<typename R::T*>(x) + row[j] * cols, col[j], cols, v);
+      }
   }
 }
 

@@ -9,16 +9,29 @@
 // HBM-bound: each matrix is read or written once; a row stays in registers
 // between its sums and its outputs.  LPR lanes hold a row, V values each: a
 // wave for rows up to 2048 columns (its sums need no LDS), 256 lanes up to
-// 8192 and 1024 above.  Statistics and sums are float32: the variance is
+// 4096 and 1024 above.  Statistics and sums are float32: the variance is
 // summed from the centred values, so nothing cancels.
 #include "layer_internal.h"
 
 namespace muon {
 namespace {
 
+// Sum over 32 or 64 lanes, the same in every lane: exchanges within rows of
+// 16 lanes, then swaps of rows and of halves (no LDS).
+template <int LANES>
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  v += __uint_as_float(dpp<kXor1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kXor2>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kMirror8>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kMirror16>(__float_as_uint(v)));
+  const uint32_t u = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  if constexpr (LANES == 64) {
+    const uint32_t t = __float_as_uint(v);
+    const auto h = __builtin_amdgcn_permlane32_swap(t, t, false, false);
+    v = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+  }
   return v;
 }
 
@@ -28,7 +41,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 template <int LPR, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float* red) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
+  for (int k = 0; k < K; ++k) v[k] = wave_sum<LPR == 32 ? 32 : 64>(v[k]);
   if constexpr (LPR > 64) {
     constexpr int W = LPR / 64;
     const int wave = threadIdx.x >> 6, first = wave / W * W;
@@ -47,51 +60,129 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* red) {
   }
 }
 
-// Rows of a block of the forward pass, and of the backward pass.
+// s / n with inv = 1 / n rounded: the quotient is corrected by its remainder.
+__device__ __forceinline__ float over(float s, float n, float inv) {
+  const float q = s * inv;
+  return __builtin_fmaf(__builtin_fmaf(-q, n, s), inv, q);
+}
+
+// 1 / sqrt(v) within half a step and a little: the hardware's estimate (one
+// step off) and a Newton correction, its residual in fused multiply-adds.
+// Tiny v is scaled up first (the estimate flushes subnormals); zero and
+// infinity give infinity and zero.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const bool tiny = v < 0x1p-96f;
+  if (tiny) v *= 0x1p96f;
+  float r = __builtin_amdgcn_rsqf(v);
+  const float t = v * r, d = __builtin_fmaf(v, r, -t);
+  const float e = __builtin_fmaf(-d, r, __builtin_fmaf(-t, r, 1.f));   // 1 - v r^2
+  const float c = __builtin_fmaf(0.5f * r, e, r);
+  r = r > 0.f && r < __builtin_inff() ? c : r;
+  return tiny ? r * 0x1p48f : r;
+}
+
+// Whether a lane holds its gains (and biases) and the next row's loads in
+// registers: not for the longest rows, whose 16 and 32 values a lane leave no
+// room for them in the 128 registers of a 1024-thread block.
+template <int LPR, int V>
+constexpr bool hold() { return LPR < 1024 || V < 16; }
+
+// Threads of a block of the forward pass, and of the backward pass.
 template <int LPR>
 constexpr int fwd_threads() { return LPR < 256 ? 256 : LPR; }
 template <int LPR>
 constexpr int bwd_threads() { return LPR < 1024 ? 512 : 1024; }
 
-template <bool BF16, int LPR, int V>
+// A sum of a parameter's gradient, to where it belongs.
+__device__ __forceinline__ void store_param(const LnBackward& p, int k, int col, float t) {
+  void* out = k ? p.dbias : p.dgain;
+  if (!out) return;
+  if (p.param_bf16) {
+    uint16_t* o = static_cast<uint16_t*>(out) + col;
+    *o = f2bf(p.accumulate ? bf2f(*o) + t : t);
+  } else {
+    float* o = static_cast<float*>(out) + col;
+    *o = p.accumulate ? *o + t : t;
+  }
+}
+
+// EVEN: cols is a multiple of a vector's N elements, so that a vector lies
+// within the row or past it.
+template <bool BF16, bool EVEN, int LPR, int V>
 __global__ __launch_bounds__(fwd_threads<LPR>()) void ln_forward_kernel(const LnForward p) {
   using R = RowVec<BF16>;
   using T = typename R::T;
   constexpr int N = R::N, NV = V / N, RPB = fwd_threads<LPR>() / LPR;
   __shared__ float red[2][fwd_threads<LPR>() / 64];
   const int lane = threadIdx.x % LPR;
-  // every lane of a block makes the same number of passes (barriers inside)
-  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < p.tokens;
-       row0 += int64_t(gridDim.x) * RPB) {
-    const int64_t row = row0 + threadIdx.x / LPR;
+  const float n = float(p.cols), inv = 1.f / n;
+  constexpr bool HOLD = hold<LPR, V>();
+  float gain[HOLD ? NV : 1][N], bias[HOLD ? NV : 1][N];
+  auto load_affine = [&](int j, float (&g)[N], float (&b)[N]) {
+    load_params<N>(p.gain, p.param_bf16, (j * LPR + lane) * N, p.cols, g);
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] = 0.f;
+    if (p.bias) load_params<N>(p.bias, p.param_bf16, (j * LPR + lane) * N, p.cols, b);
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_affine(j, gain[j], bias[j]);
+  }
+  const int64_t stride = int64_t(gridDim.x) * RPB;
+  auto load = [&](int64_t row, u32x4_t (&w)[NV]) {
+    const T* x = static_cast<const T*>(p.x) + (row < p.tokens ? row : p.tokens - 1) * p.ldx;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) w[j] = load_raw<BF16, EVEN>(x, (j * LPR + lane) * N, p.cols);
+  };
+  u32x4_t next[HOLD ? NV : 1];
+  const int64_t first = int64_t(blockIdx.x) * RPB + threadIdx.x / LPR;
+  if constexpr (HOLD) load(first, next);
+  // every lane of a block makes the same number of passes (barriers inside);
+  // the next row is on its way while one is worked on
+  for (int64_t row = first; row - threadIdx.x / LPR < p.tokens; row += stride) {
     const bool live = row < p.tokens;
-    const T* x = static_cast<const T*>(p.x) + (live ? row : p.tokens - 1) * p.ldx;
+    u32x4_t w[NV];
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) w[j] = next[j];
+      if (row - threadIdx.x / LPR + stride < p.tokens) load(row + stride, next);
+    } else {
+      load(row, w);
+    }
     float v[NV][N];
     float s[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load_vec<BF16>(x, (j * LPR + lane) * N, p.cols, v[j]);
+      unpack_raw<BF16>(w[j], v[j]);
 #pragma unroll
       for (int i = 0; i < N; ++i) s[0] += v[j][i];
     }
     row_sum<LPR, 1>(s, red[0]);
-    const float mean = s[0] * p.inv_cols;
+    const float mean = over(s[0], n, inv);
     if (p.xc.fmt >= 0 && live) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) ckpt_store<N>(p.xc, row, (j * LPR + lane) * N, p.cols, v[j]);
+      for (int j = 0; j < NV; ++j) ckpt_store<BF16>(p.xc, row, (j * LPR + lane) * N, p.cols, w[j]);
     }
     float q[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int left = p.cols - (j * LPR + lane) * N;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        v[j][i] = i < left ? v[j][i] - mean : 0.f;
-        q[0] = __builtin_fmaf(v[j][i], v[j][i], q[0]);
+      for (int i = 0; i < N; ++i) v[j][i] -= mean;
+      float t = 0.f;
+      if constexpr (!EVEN) {
+        if (left < N) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (i >= left) v[j][i] = 0.f;
+        }
       }
+#pragma unroll
+      for (int i = 0; i < N; ++i) t = __builtin_fmaf(v[j][i], v[j][i], t);
+      q[0] += left > 0 ? t : 0.f;
     }
     row_sum<LPR, 1>(q, red[1]);
-    const float rstd = 1.f / __builtin_sqrtf(q[0] * p.inv_cols + p.eps);
+    const float rstd = inv_sqrt(over(q[0], n, inv) + p.eps);
     if (!live) continue;
     if (lane == 0) {
       p.mean[row] = mean;
@@ -101,33 +192,24 @@ __global__ __launch_bounds__(fwd_threads<LPR>()) void ln_forward_kernel(const Ln
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int col = (j * LPR + lane) * N;
-      float g[N], b[N];
-      load_params<N>(p.gain, p.param_bf16, col, p.cols, g);
-      if (p.bias) {
-        load_params<N>(p.bias, p.param_bf16, col, p.cols, b);
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) b[i] = 0.f;
-      }
       float o[N];
+      if constexpr (!HOLD) load_affine(j, gain[0], bias[0]);
+      const int k = HOLD ? j : 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(v[j][i] * rstd, g[i], b[i]);
-      store_vec<BF16>(y, col, p.cols, o);
+      for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(v[j][i] * rstd, gain[k][i], bias[k][i]);
+      u32x4_t out = pack_raw<BF16>(o);
+      store_raw<BF16, EVEN>(y, col, p.cols, out);
+      // the checkpoint holds y as the next layer reads it
       if (p.yc.fmt >= 0) {
-        // the checkpoint holds y as the next layer reads it
-        const int left = p.cols - col;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if constexpr (BF16) o[i] = bf2f(f2bf(o[i]));
-          if (i >= left) o[i] = 0.f;
-        }
-        ckpt_store<N>(p.yc, row, col, p.cols, o);
+        if (col >= p.cols) out = u32x4_t{0, 0, 0, 0};
+        ckpt_store<BF16>(p.yc, row, col, p.cols, out);
       }
     }
   }
 }
 
-template <bool BF16, int LPR, int V>
+// CK: x from its checkpoint.
+template <bool BF16, bool EVEN, bool CK, int LPR, int V>
 __global__ __launch_bounds__(bwd_threads<LPR>()) void ln_backward_kernel(const LnBackward p) {
   using R = RowVec<BF16>;
   using T = typename R::T;
@@ -135,65 +217,101 @@ __global__ __launch_bounds__(bwd_threads<LPR>()) void ln_backward_kernel(const L
   __shared__ float red[2][2 * NT / 64];
   __shared__ float join[RPB > 1 ? RPB : 1][RPB > 1 ? LPR * N : 1];
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
-  float dg[NV][N], db[NV][N], gain[NV][N];
+  const float n = float(p.cols), inv = 1.f / n;
+  constexpr bool HOLD = hold<LPR, V>();
+  float dg[NV][N], db[NV][N], gain[HOLD ? NV : 1][N];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    load_params<N>(p.gain, p.param_bf16, (j * LPR + lane) * N, p.cols, gain[j]);
+    if constexpr (HOLD) load_params<N>(p.gain, p.param_bf16, (j * LPR + lane) * N, p.cols, gain[j]);
 #pragma unroll
     for (int i = 0; i < N; ++i) dg[j][i] = db[j][i] = 0.f;
   }
-  int turn = 0;
-  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < p.tokens;
-       row0 += int64_t(gridDim.x) * RPB) {
-    const int64_t row = row0 + sub;
-    const bool live = row < p.tokens;
-    const int64_t at = live ? row : p.tokens - 1;
-    const float mean = p.mean[at], rstd = p.rstd[at];
-    const T* dy = static_cast<const T*>(p.dy) + at * p.lddy;
-    float a[NV][N], xh[NV][N];
-    float s[2] = {0.f, 0.f};
+  // A row's loads; the next row's are on their way while one is worked on.
+  struct Row {
+    u32x4_t dy[NV];
+    u32x4_t x[CK ? 1 : NV];
+    CkptVec<N> c[CK ? NV : 1];
+    float mean, rstd;
+  } next;
+  auto load = [&](int64_t row, Row& r) {
+    const int64_t at = row < p.tokens ? row : p.tokens - 1;
+    r.mean = p.mean[at];
+    r.rstd = p.rstd[at];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int col = (j * LPR + lane) * N;
-      load_vec<BF16>(dy, col, p.cols, a[j]);
-      if (p.x)
-        load_vec<BF16>(static_cast<const T*>(p.x) + at * p.ldx, col, p.cols, xh[j]);
+      r.dy[j] = load_raw<BF16, EVEN>(static_cast<const T*>(p.dy) + at * p.lddy, col, p.cols);
+      if constexpr (CK)
+        r.c[j] = ckpt_load<N>(p.xc, at, col);
       else
-        ckpt_load<N>(p.xc, at, col, xh[j]);
+        r.x[j] = load_raw<BF16, EVEN>(static_cast<const T*>(p.x) + at * p.ldx, col, p.cols);
     }
+  };
+  const int64_t stride = int64_t(gridDim.x) * RPB;
+  if constexpr (HOLD) load(int64_t(blockIdx.x) * RPB + sub, next);
+  int turn = 0;
+  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < p.tokens; row0 += stride) {
+    const int64_t row = row0 + sub;
+    const bool live = row < p.tokens;
+    Row cur;
+    if constexpr (HOLD) {
+      cur = next;
+      if (row0 + stride < p.tokens) load(row + stride, next);
+    } else {
+      load(row, cur);
+    }
+    float a[NV][N], xh[NV][N];
+    float s[2] = {0.f, 0.f};
+    // past the row's end dy is zero, and so is every term of the sums
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int left = p.cols - (j * LPR + lane) * N;
+      unpack_raw<BF16>(cur.dy[j], a[j]);
+      if constexpr (CK)
+        ckpt_values<N>(cur.c[j], p.xc.fmt, xh[j]);
+      else
+        unpack_raw<BF16>(cur.x[j], xh[j]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) xh[j][i] = (xh[j][i] - cur.mean) * cur.rstd;
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          dg[j][i] = __builtin_fmaf(a[j][i], xh[j][i], dg[j][i]);
+          db[j][i] += a[j][i];
+        }
+      }
+      const int k = HOLD ? j : 0;
+      if constexpr (!HOLD) load_params<N>(p.gain, p.param_bf16, (j * LPR + lane) * N, p.cols, gain[0]);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float d = a[j][i];
-        const float h = i < left ? (xh[j][i] - mean) * rstd : 0.f;
-        if (live) {
-          dg[j][i] = __builtin_fmaf(d, h, dg[j][i]);
-          db[j][i] += d;
-        }
-        xh[j][i] = h;
-        a[j][i] = d * gain[j][i];
+        a[j][i] *= gain[k][i];
         s[0] += a[j][i];
-        s[1] = __builtin_fmaf(a[j][i], h, s[1]);
+        s[1] = __builtin_fmaf(a[j][i], xh[j][i], s[1]);
       }
     }
     row_sum<LPR, 2>(s, red[turn]);
     turn ^= 1;
     if (live) {
-      const float c0 = s[0] * p.inv_cols, c1 = s[1] * p.inv_cols;
+      const float c0 = over(s[0], n, inv), c1 = over(s[1], n, inv);
       T* dx = static_cast<T*>(p.dx) + row * p.cols;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float o[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = rstd * (a[j][i] - c0 - xh[j][i] * c1);
-        store_vec<BF16>(dx, (j * LPR + lane) * N, p.cols, o);
+        for (int i = 0; i < N; ++i) o[i] = cur.rstd * (a[j][i] - c0 - xh[j][i] * c1);
+        store_raw<BF16, EVEN>(dx, (j * LPR + lane) * N, p.cols, pack_raw<BF16>(o));
       }
     }
   }
-  // One row of partial sums per block: the block's rows are added in order.
+  // One row of partial sums per block, the block's rows added in order; a
+  // single block's are the gradients.
   float* out = p.partial + int64_t(blockIdx.x) * 2 * p.cols;
+  auto put = [&](int k, int col, float t) {
+    if (col >= p.cols) return;
+    if (p.blocks == 1)
+      store_param(p, k, col, t);
+    else
+      out[k * p.cols + col] = t;
+  };
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -208,15 +326,11 @@ __global__ __launch_bounds__(bwd_threads<LPR>()) void ln_backward_kernel(const L
           float t = 0.f;
 #pragma unroll
           for (int r = 0; r < RPB; ++r) t += join[r][c];
-          const int col = j * LPR * N + c;
-          if (col < p.cols) out[k * p.cols + col] = t;
+          put(k, j * LPR * N + c, t);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int col = (j * LPR + lane) * N + i;
-          if (col < p.cols) out[k * p.cols + col] = acc[i];
-        }
+        for (int i = 0; i < N; ++i) put(k, (j * LPR + lane) * N + i, acc[i]);
       }
     }
   }
@@ -231,7 +345,7 @@ __global__ __launch_bounds__(1024) void ln_params_kernel(const LnBackward p) {
   float t = 0.f;
   if (col < p.cols) {
     const float* in = p.partial + int64_t(k) * p.cols + col;
-#pragma unroll 4
+#pragma unroll 16
     for (int b = ty; b < p.blocks; b += 32) t += in[int64_t(b) * 2 * p.cols];
   }
   part[ty][tx] = t;
@@ -240,25 +354,24 @@ __global__ __launch_bounds__(1024) void ln_params_kernel(const LnBackward p) {
     t = 0.f;
 #pragma unroll
     for (int r = 0; r < 32; ++r) t += part[r][tx];
-    void* out = k ? p.dbias : p.dgain;
-    if (p.param_bf16) {
-      uint16_t* o = static_cast<uint16_t*>(out) + col;
-      *o = f2bf(p.accumulate ? bf2f(*o) + t : t);
-    } else {
-      float* o = static_cast<float*>(out) + col;
-      *o = p.accumulate ? *o + t : t;
-    }
+    store_param(p, k, col, t);
   }
 }
 
-// Lanes and values per lane of a row.
+// Lanes and values per lane of a row: the least that hold it.  Three vectors a
+// lane in half a wave fit rows of 768 (forward 20.1 -> 15.7 us at 16384 rows in
+// bf16), but cost the backward more registers than they save lanes (20.4
+// -> 23.2); a wave of three vectors a lane for 1411 float32 columns was slower
+// than 256 lanes of two in both (18.9 against 17.1, 24.0 against 19.8).
 struct RowShape {
   int lpr, v;
 };
-RowShape row_shape(int64_t cols) {
-  const int lpr = cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024;
-  const int64_t per_lane = (cols + lpr - 1) / lpr;
-  return {lpr, per_lane <= 8 ? 8 : per_lane <= 16 ? 16 : 32};
+RowShape row_shape(int64_t cols, bool backward) {
+  constexpr RowShape all[] = {{32, 8}, {64, 8}, {32, 24}, {64, 16}, {256, 8},
+                              {256, 16}, {1024, 8}, {1024, 16}, {1024, 32}};
+  for (const RowShape& r : all)
+    if (cols <= r.lpr * r.v && !(backward && r.v == 24)) return r;
+  return all[8];
 }
 
 template <bool BF16, int LPR, int V>
@@ -266,46 +379,61 @@ hipError_t forward(const LnForward& p, hipStream_t s) {
   constexpr int NT = fwd_threads<LPR>(), RPB = NT / LPR;
   const int64_t want = (p.tokens + RPB - 1) / RPB;
   const int64_t cap = 256 * (2048 / NT);   // the waves that fill the chip
-  hipLaunchKernelGGL((ln_forward_kernel<BF16, LPR, V>), dim3(unsigned(want < cap ? want : cap)),
-                     dim3(NT), 0, s, p);
+  const dim3 grid(unsigned(want < cap ? want : cap)), block(NT);
+  if (p.cols % RowVec<BF16>::N == 0)
+    hipLaunchKernelGGL((ln_forward_kernel<BF16, true, LPR, V>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((ln_forward_kernel<BF16, false, LPR, V>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
+template <bool BF16, bool EVEN, int LPR, int V>
+hipError_t backward_of(const LnBackward& p, hipStream_t s) {
+  const dim3 grid(unsigned(p.blocks)), block(bwd_threads<LPR>());
+  if (p.x)
+    hipLaunchKernelGGL((ln_backward_kernel<BF16, EVEN, false, LPR, V>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((ln_backward_kernel<BF16, EVEN, true, LPR, V>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
 template <bool BF16, int LPR, int V>
 hipError_t backward(const LnBackward& p, hipStream_t s) {
-  hipLaunchKernelGGL((ln_backward_kernel<BF16, LPR, V>), dim3(unsigned(p.blocks)),
-                     dim3(bwd_threads<LPR>()), 0, s, p);
-  return hipGetLastError();
+  return p.cols % RowVec<BF16>::N == 0 ? backward_of<BF16, true, LPR, V>(p, s)
+                                       : backward_of<BF16, false, LPR, V>(p, s);
 }
 
 }  // namespace
 
-// Two blocks of 512 threads per CU, or one of 1024.
+// Two blocks of 512 threads per CU, or one of 1024.  Up to kOneBlock passes of
+// a block are left to a single one, which spares the second launch.
+constexpr int64_t kOneBlock = 4;
 int ln_backward_blocks(int64_t tokens, int64_t cols) {
-  const int lpr = row_shape(cols).lpr, nt = lpr < 1024 ? 512 : 1024;
+  const int lpr = row_shape(cols, true).lpr, nt = lpr < 1024 ? 512 : 1024;
   const int64_t want = (tokens + nt / lpr - 1) / (nt / lpr);
   const int64_t cap = 256 * (1024 / nt);
-  return int(want < cap ? want : cap);
+  return int(want < 1 ? 0 : want <= kOneBlock ? 1 : want < cap ? want : cap);
 }
 
-#define MUON_LN_SHAPES(CALL)                                   \
-  const RowShape r = row_shape(p.cols);                        \
-  if (r.lpr == 64) {                                           \
-    if (r.v == 8) return bf16 ? CALL<true, 64, 8>(p, s) : CALL<false, 64, 8>(p, s);     \
-    if (r.v == 16) return bf16 ? CALL<true, 64, 16>(p, s) : CALL<false, 64, 16>(p, s);  \
-    return bf16 ? CALL<true, 64, 32>(p, s) : CALL<false, 64, 32>(p, s);                 \
-  }                                                            \
-  if (r.lpr == 256) {                                          \
-    if (r.v == 16) return bf16 ? CALL<true, 256, 16>(p, s) : CALL<false, 256, 16>(p, s); \
-    return bf16 ? CALL<true, 256, 32>(p, s) : CALL<false, 256, 32>(p, s);               \
-  }                                                            \
-  if (r.v == 16) return bf16 ? CALL<true, 1024, 16>(p, s) : CALL<false, 1024, 16>(p, s); \
-  return bf16 ? CALL<true, 1024, 32>(p, s) : CALL<false, 1024, 32>(p, s)
+#define MUON_LN_SHAPE(CALL, LPR, V) \
+  if (r.lpr == LPR && r.v == V) return bf16 ? CALL<true, LPR, V>(p, s) : CALL<false, LPR, V>(p, s)
+#define MUON_LN_SHAPES(CALL)              \
+  MUON_LN_SHAPE(CALL, 32, 8);             \
+  MUON_LN_SHAPE(CALL, 64, 8);             \
+  MUON_LN_SHAPE(CALL, 64, 16);            \
+  MUON_LN_SHAPE(CALL, 256, 8);            \
+  MUON_LN_SHAPE(CALL, 256, 16);           \
+  MUON_LN_SHAPE(CALL, 1024, 8);           \
+  MUON_LN_SHAPE(CALL, 1024, 16);          \
+  MUON_LN_SHAPE(CALL, 1024, 32);          \
+  return hipErrorInvalidValue
 
 hipError_t launch_ln_forward(const LnForward& p, bool bf16, hipStream_t s) {
+  const RowShape r = row_shape(p.cols, false);
+  MUON_LN_SHAPE(forward, 32, 24);
   MUON_LN_SHAPES(forward);
 }
 hipError_t launch_ln_backward(const LnBackward& p, bool bf16, hipStream_t s) {
+  const RowShape r = row_shape(p.cols, true);
   MUON_LN_SHAPES(backward);
 }
 

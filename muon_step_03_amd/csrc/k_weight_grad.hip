@@ -26,8 +26,6 @@ namespace {
 constexpr int BM = 128, BN = 128, BK = 32;   // rows of G, columns of G, tokens
 constexpr int kThreads = 256;                // 2 x 2 waves of 64 x 64
 
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-
 // A piece: tokens [begin, end) of matrix e; slot: its place among the partial
 // sums (parts > 1).  In the table of a ragged call, e < 0 marks no piece.
 struct Piece {

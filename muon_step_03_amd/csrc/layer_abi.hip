@@ -189,7 +189,6 @@ int muon_layernorm_forward(const void* x, int64_t ldx, const void* gain, const v
   p.cols = int(cols);
   p.param_bf16 = param_dtype == MUON_DTYPE_BF16;
   p.eps = float(eps);
-  p.inv_cols = float(1.0 / double(cols));
   p.xc = view(x_ckpt);
   p.yc = view(y_ckpt);
   Trace t("muon_layernorm_forward");
@@ -253,12 +252,11 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
   p.param_bf16 = param_dtype == MUON_DTYPE_BF16;
   p.accumulate = accumulate != 0;
   p.blocks = ln_backward_blocks(tokens, cols);
-  p.inv_cols = float(1.0 / double(cols));
   Trace t("muon_layernorm_backward");
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (p.blocks > 0) {
     const int st = launched(launch_ln_backward(p, dtype == MUON_DTYPE_BF16, s), "layernorm_backward", s);
-    if (st != MUON_OK) return st;
+    if (st != MUON_OK || p.blocks == 1) return st;
   }
   return launched(launch_ln_params(p, s), "layernorm_params", s);
 }

@@ -48,28 +48,6 @@ __device__ __forceinline__ float ckpt_up(int byte) {
   return __uint_as_float(byte == 255 ? 0x7fc00000u : uint32_t(byte) << 23);
 }
 
-// Four values -> four q bytes.  A marked block's values are not finite, so
-// they are replaced, not multiplied, by zero.
-__device__ __forceinline__ uint32_t ckpt_pack4(const float* v, float down, int fmt) {
-  float s[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = down == 0.f ? 0.f : v[i] * down;
-  if (fmt == MUON_CKPT_E4M3) {
-    // only values that the largest exponent cannot hold are clamped
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = __builtin_amdgcn_fmed3f(s[i], -448.f, 448.f);
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(s[0], s[1], 0, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(s[2], s[3], w, true);
-    return uint32_t(w);
-  }
-  // adding 1.5 * 2^23 leaves the integer, rounded half to even, in the low byte
-  uint32_t b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    b[i] = __float_as_uint(__builtin_amdgcn_fmed3f(s[i], -127.f, 127.f) + 12582912.f) & 0xffu;
-  return b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
-}
-
 // Four q bytes -> four values, exact.
 __device__ __forceinline__ void ckpt_unpack4(uint32_t w, float up, int fmt, float* v) {
   if (fmt == MUON_CKPT_E4M3) {
@@ -105,28 +83,73 @@ struct RowVec<false> {
   static constexpr int N = 4;
 };
 
-// Elements [col, col + N) of a row of `cols`, those past its end as zero.
-template <bool BF16>
-__device__ __forceinline__ void load_vec(const void* row, int col, int cols, float* v) {
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// The 16 bytes of elements [col, col + N) of a row of `cols`, those past its
+// end as zero.  EVEN: cols is a multiple of N, so no vector crosses the end.
+template <bool BF16, bool EVEN = false>
+__device__ __forceinline__ u32x4_t load_raw(const void* row, int col, int cols) {
   using R = RowVec<BF16>;
   using T = typename R::T;
   const T* p = static_cast<const T*>(row) + col;
+  u32x4_t w = {0, 0, 0, 0};
   if (col + R::N <= cols) {
-    const typename R::Raw w = *reinterpret_cast<const typename R::Raw*>(p);
-    if constexpr (BF16) {
+    const typename R::Raw r = *reinterpret_cast<const typename R::Raw*>(p);
+    w = u32x4_t{r[0], r[1], r[2], r[3]};
+  } else if constexpr (!EVEN) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < R::N; ++i)
+      if (col + i < cols) {
+        if constexpr (BF16)
+          w[i / 2] |= uint32_t(p[i]) << (16 * (i & 1));
+        else
+          w[i] = __float_as_uint(p[i]);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < R::N; ++i) v[i] = col + i < cols ? Elem<BF16>::load(p + i) : 0.f;
   }
+  return w;
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack_raw(u32x4_t w, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      v[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ u32x4_t pack_raw(const float* v) {
+  u32x4_t w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = BF16 ? f2bf2(v[2 * i], v[2 * i + 1]) : __float_as_uint(v[i]);
+  return w;
+}
+template <bool BF16, bool EVEN = false>
+__device__ __forceinline__ void store_raw(void* row, int col, int cols, u32x4_t w) {
+  using R = RowVec<BF16>;
+  using T = typename R::T;
+  T* p = static_cast<T*>(row) + col;
+  if (col + R::N <= cols) {
+    *reinterpret_cast<typename R::Raw*>(p) = typename R::Raw{w[0], w[1], w[2], w[3]};
+  } else if constexpr (!EVEN) {
+#pragma unroll
+    for (int i = 0; i < R::N; ++i)
+      if (col + i < cols) {
+        if constexpr (BF16)
+          p[i] = uint16_t(w[i / 2] >> (16 * (i & 1)));
+        else
+          p[i] = __uint_as_float(w[i]);
+      }
+  }
+}
+
+// Elements [col, col + N) of a row of `cols`, those past its end as zero.
+template <bool BF16>
+__device__ __forceinline__ void load_vec(const void* row, int col, int cols, float* v) {
+  unpack_raw<BF16>(load_raw<BF16>(row, col, cols), v);
 }
 
 // The same for `n` = BF16 ? 8 : 4 values starting at any column, of either
@@ -150,76 +173,134 @@ __device__ __forceinline__ void load_params(const void* base, bool bf16, int col
 
 template <bool BF16>
 __device__ __forceinline__ void store_vec(void* row, int col, int cols, const float* v) {
-  using R = RowVec<BF16>;
-  using T = typename R::T;
-  T* p = static_cast<T*>(row) + col;
-  if (col + R::N <= cols) {
-    typename R::Raw w;
-    if constexpr (BF16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = f2bf2(v[2 * i], v[2 * i + 1]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
-    }
-    *reinterpret_cast<typename R::Raw*>(p) = w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < R::N; ++i)
-      if (col + i < cols) p[i] = Elem<BF16>::cvt(v[i]);
-  }
+  store_raw<BF16>(row, col, cols, pack_raw<BF16>(v));
 }
 
-// Quantises the N values of this lane at columns [col, col + N) of a row;
-// the 32 / N consecutive lanes that hold a block take part together.  The
-// lanes past the row's end write the padding (q and scale zero).
-template <int N>
+// Lane exchanges within a row of 16 lanes (data-parallel-primitive moves).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, false));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E;             // quad_perm
+constexpr int kMirror8 = 0x141, kMirror16 = 0x140;    // row_half_mirror, row_mirror
+
+// Quantises a vector of 16 bytes at columns [col, col + N) of a row; the 32 / N
+// consecutive lanes that hold a block take part together.  The lanes past
+// the row's end (their elements zero) write the padding.
+template <bool BF16>
 __device__ __forceinline__ void ckpt_store(const Ckpt& c, int64_t row, int col, int cols,
-                                           const float* v) {
-  uint32_t a = 0;
+                                           u32x4_t w) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  constexpr int N = RowVec<BF16>::N;
+  // the block's largest magnitude as a bit pattern (the order of floats is
+  // that of their patterns)
+  uint32_t a;
+  if constexpr (BF16) {
+    u16x2 m = __builtin_bit_cast(u16x2, w[0] & 0x7fff7fffu);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-    a = a > b ? a : b;
-  }
+    for (int i = 1; i < 4; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+    a = uint32_t(m[0] > m[1] ? m[0] : m[1]) << 16;
+  } else {
+    a = w[0] & 0x7fffffffu;
 #pragma unroll
-  for (int off = 1; off < MUON_CKPT_BLOCK / N; off <<= 1) {
-    const uint32_t b = __shfl_xor(a, off, 64);
-    a = a > b ? a : b;
+    for (int i = 1; i < 4; ++i) a = max(a, w[i] & 0x7fffffffu);
   }
+  a = max(a, dpp<kXor1>(a));
+  a = max(a, dpp<kXor2>(a));
+  if constexpr (N == 4) a = max(a, dpp<kMirror8>(a));
   const int byte = ckpt_scale_byte(a, c.fmt);
-  const float down = ckpt_down(byte);
-  if (col < c.q_pitch) {
-    uint32_t* q = reinterpret_cast<uint32_t*>(c.q + row * c.q_pitch + col);
-    if constexpr (N == 8) {
-      const uint2 w = {ckpt_pack4(v, down, c.fmt), ckpt_pack4(v + 4, down, c.fmt)};
-      *reinterpret_cast<uint2*>(q) = w;
-    } else {
-      *q = ckpt_pack4(v, down, c.fmt);
+  const int top = 127 + (c.fmt == MUON_CKPT_E4M3 ? kCkptEMaxE4m3 : kCkptEMaxInt8);
+  uint32_t q[N / 4];
+  if (c.fmt == MUON_CKPT_E4M3 && byte != top) {
+    // the conversion divides by 2^e and rounds to nearest even: in range here
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    const float up = __uint_as_float(uint32_t(byte) << 23);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      s16x2 r = {0, 0};
+      if constexpr (BF16) {
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, uint32_t(w[2 * i])), up, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, uint32_t(w[2 * i + 1])), up, true);
+      } else {
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(w[0]), __uint_as_float(w[1]), up, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(w[2]), __uint_as_float(w[3]), up, true);
+      }
+      q[i] = __builtin_bit_cast(uint32_t, r);
     }
+  } else {
+    // at the largest exponent a value may still be out of range: it saturates
+    const float down = ckpt_down(byte);
+    float v[N];
+    unpack_raw<BF16>(w, v);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float* x = v + 4 * i;
+      if (c.fmt == MUON_CKPT_E4M3) {
+        int r = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_fmed3f(x[0] * down, -448.f, 448.f),
+                                                __builtin_amdgcn_fmed3f(x[1] * down, -448.f, 448.f), 0, false);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_fmed3f(x[2] * down, -448.f, 448.f),
+                                            __builtin_amdgcn_fmed3f(x[3] * down, -448.f, 448.f), r, true);
+        q[i] = uint32_t(r);
+      } else {
+        // adding 1.5 * 2^23 leaves the integer, rounded half to even, in the
+        // low byte; the clamp only acts at the largest exponent
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          b[j] = __float_as_uint(__builtin_amdgcn_fmed3f(x[j] * down, -127.f, 127.f) + 12582912.f);
+        const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+        q[i] = lo | hi;
+      }
+    }
+  }
+  if (byte == 255) {   // a marked block
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) q[i] = 0;
+  }
+  if (col < c.q_pitch) {
+    uint32_t* to = reinterpret_cast<uint32_t*>(c.q + row * c.q_pitch + col);
+    if constexpr (N == 8)
+      *reinterpret_cast<uint2*>(to) = uint2{q[0], q[1]};
+    else
+      *to = q[0];
   }
   if (col % MUON_CKPT_BLOCK == 0 && col / MUON_CKPT_BLOCK < c.s_pitch)
     c.scale[row * c.s_pitch + col / MUON_CKPT_BLOCK] = uint8_t(col < cols ? byte : 0);
 }
 
-// N values of a checkpoint's row from column `col` on (a multiple of N; zero
-// past the row's pitch).
+// N = 8 or 4 values of a checkpoint's row from column `col` on (a multiple of
+// N; zero past the row's pitch): loaded, then brought back.
 template <int N>
-__device__ __forceinline__ void ckpt_load(const Ckpt& c, int64_t row, int col, float* v) {
+struct CkptVec {
+  uint32_t w[N / 4];
+  int byte;
+};
+template <int N>
+__device__ __forceinline__ CkptVec<N> ckpt_load(const Ckpt& c, int64_t row, int col) {
+  CkptVec<N> r;
+  r.byte = 0;
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) r.w[i] = 0;
   if (col < c.q_pitch) {
-    const float up = ckpt_up(c.scale[row * c.s_pitch + col / MUON_CKPT_BLOCK]);
+    r.byte = c.scale[row * c.s_pitch + col / MUON_CKPT_BLOCK];
     const uint32_t* q = reinterpret_cast<const uint32_t*>(c.q + row * c.q_pitch + col);
     if constexpr (N == 8) {
       const uint2 w = *reinterpret_cast<const uint2*>(q);
-      ckpt_unpack4(w.x, up, c.fmt, v);
-      ckpt_unpack4(w.y, up, c.fmt, v + 4);
+      r.w[0] = w.x;
+      r.w[1] = w.y;
     } else {
-      ckpt_unpack4(*q, up, c.fmt, v);
+      r.w[0] = *q;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.f;
   }
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void ckpt_values(const CkptVec<N>& r, int fmt, float* v) {
+  const float up = ckpt_up(r.byte);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) ckpt_unpack4(r.w[i], up, fmt, v + 4 * i);
 }
 
 // ------------------------------------------------------------- layer norm
@@ -235,7 +316,6 @@ struct LnForward {
   int cols;
   int param_bf16;
   float eps;
-  float inv_cols;
   Ckpt xc, yc;          // checkpoints of x and y to write (fmt < 0: none)
 };
 
@@ -257,7 +337,6 @@ struct LnBackward {
   int param_bf16;
   int accumulate;
   int blocks;           // of the first launch (0: no tokens)
-  float inv_cols;
 };
 
 // Blocks of the backward's first launch: each leaves one row of partial sums.

@@ -15,8 +15,8 @@ uses tensors across streams orders them, as with any PyTorch operator.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -29,19 +29,25 @@ _FORMAT_CODES = {torch.float8_e4m3fn: _lib.MUON_CKPT_E4M3, torch.int8: _lib.MUON
 _FORMAT_NAMES = {v: k for k, v in FORMATS.items()}
 
 
-def _scope(stream, device):
-    """Makes ``device`` (and ``stream``, if given) current for a call."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle, no object
 
 
-def _stream_of(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _on_device(fn):
+    """Runs ``fn(x, ...)`` with the device of its first argument (a tensor or
+    an ActCheckpoint) current, on the stream given as ``stream``."""
+    @functools.wraps(fn)
+    def call(x, *args, stream=None, **kw):
+        device = getattr(x, "device", None)
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            with torch.cuda.stream(stream):
+                return fn(x, *args, **kw)
+        if device is not None and device.type == "cuda" and device.index != torch.cuda.current_device():
+            with torch.cuda.device(device):
+                return fn(x, *args, **kw)
+        return fn(x, *args, **kw)
+    return call
 
 
 def _check_rows(name, t, device=None, shape=None, dtype=None, contiguous=False):
@@ -97,7 +103,7 @@ class ActCheckpoint:
     float8_e4m3fn or int8, ``scale`` uint8 [tokens, blocks of 32 columns up to
     a multiple of 4].  An element stands for ``q * 2^(scale - 127)``."""
 
-    __slots__ = ("q", "scale", "cols", "_c")
+    __slots__ = ("_q", "_scale", "_cols", "_code")
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor, cols: int):
         if q.dtype not in _FORMAT_CODES:
@@ -112,8 +118,7 @@ class ActCheckpoint:
                                  f"{(tokens, pitch)} for {cols} columns, got {tuple(t.shape)}")
         if scale.device != q.device:
             raise ValueError(f"scale is on {scale.device}, q on {q.device}")
-        self.q, self.scale, self.cols = q, scale, cols
-        self._c = _lib.Ckpt(q.data_ptr(), scale.data_ptr(), tokens, cols, _FORMAT_CODES[q.dtype])
+        self._q, self._scale, self._cols, self._code = q, scale, cols, _FORMAT_CODES[q.dtype]
 
     @classmethod
     def empty(cls, tokens: int, cols: int, fmt: str = "e4m3", device="cuda") -> "ActCheckpoint":
@@ -123,25 +128,40 @@ class ActCheckpoint:
         except KeyError:
             raise ValueError(f"unknown checkpoint format {fmt!r}; expected one of "
                              f"{sorted(FORMATS)}") from None
-        return cls(torch.empty(tokens, _lib.ckpt_q_pitch(cols), dtype=store, device=device),
-                   torch.empty(tokens, _lib.ckpt_scale_pitch(cols), dtype=torch.uint8,
-                               device=device), cols)
+        ck = cls.__new__(cls)
+        ck._q = torch.empty((tokens, _lib.ckpt_q_pitch(cols)), dtype=store, device=device)
+        ck._scale = torch.empty((tokens, _lib.ckpt_scale_pitch(cols)), dtype=torch.uint8,
+                                device=device)
+        ck._cols, ck._code = cols, _FORMAT_CODES[store]
+        return ck
+
+    @property
+    def q(self) -> torch.Tensor:
+        return self._q
+
+    @property
+    def scale(self) -> torch.Tensor:
+        return self._scale
+
+    @property
+    def cols(self) -> int:
+        return self._cols
 
     @property
     def tokens(self) -> int:
-        return self.q.shape[0]
+        return self._q.shape[0]
 
     @property
     def shape(self):
-        return (self.tokens, self.cols)
+        return (self._q.shape[0], self._cols)
 
     @property
     def format(self) -> str:
-        return _FORMAT_NAMES[self.q.dtype]
+        return _FORMAT_NAMES[self._q.dtype]
 
     @property
     def device(self) -> torch.device:
-        return self.q.device
+        return self._q.device
 
     @property
     def nbytes(self) -> int:
@@ -165,35 +185,37 @@ def _as_checkpoint(name, spec, shape, device) -> Optional[ActCheckpoint]:
 
 
 def _ref(ck):
-    return None if ck is None else ctypes.byref(ck._c)
+    if ck is None:
+        return None
+    return ctypes.byref(_lib.Ckpt(ck._q.data_ptr(), ck._scale.data_ptr(), ck._q.shape[0], ck._cols,
+                                  ck._code))
 
 
-def checkpoint_save(x: torch.Tensor, fmt: str = "e4m3", *, out: Optional[ActCheckpoint] = None,
-                    stream=None) -> ActCheckpoint:
+@_on_device
+def checkpoint_save(x: torch.Tensor, fmt: str = "e4m3", *, out: Optional[ActCheckpoint] = None) -> ActCheckpoint:
     """Keeps ``x`` [tokens, cols] in 8 bits, ``fmt`` "e4m3" or "int8" (or in
     the format of ``out``)."""
     ld = _check_rows("x", x)
     dt = dtype_code(x.dtype)
-    with _scope(stream, x.device):
-        ck = _as_checkpoint("out", fmt if out is None else out, tuple(x.shape), x.device)
-        st = _lib.lib().muon_checkpoint_save(x.data_ptr(), ld, dt, _ref(ck), _stream_of(x.device))
+    ck = _as_checkpoint("out", fmt if out is None else out, tuple(x.shape), x.device)
+    st = _lib.lib().muon_checkpoint_save(x.data_ptr(), ld, dt, _ref(ck), _raw_stream(x.device.index))
     _check(st, "muon_checkpoint_save")
     return ck
 
 
+@_on_device
 def checkpoint_restore(ck: ActCheckpoint, dtype: torch.dtype = torch.bfloat16, *,
-                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values a checkpoint stands for (exact in bfloat16 and float32)."""
     if not isinstance(ck, ActCheckpoint):
         raise TypeError("ck must be an ActCheckpoint")
     dt = dtype_code(dtype if out is None else out.dtype)
-    with _scope(stream, ck.device):
-        if out is None:
-            out = torch.empty(ck.shape, dtype=dtype, device=ck.device)
-        else:
-            _check_rows("out", out, ck.device, ck.shape, contiguous=True)
-        st = _lib.lib().muon_checkpoint_restore(_ref(ck), out.data_ptr(), dt,
-                                                _stream_of(ck.device))
+    if out is None:
+        out = torch.empty(ck.shape, dtype=dtype, device=ck.device)
+    else:
+        _check_rows("out", out, ck.device, ck.shape, contiguous=True)
+    st = _lib.lib().muon_checkpoint_restore(_ref(ck), out.data_ptr(), dt,
+                                            _raw_stream(ck.device.index))
     _check(st, "muon_checkpoint_restore")
     return out
 
@@ -206,8 +228,8 @@ class LayerNormOut(NamedTuple):
     y_checkpoint: Optional[ActCheckpoint]
 
 
-def layernorm_forward(x, gain, bias=None, *, eps=1e-5, x_checkpoint=None, y_checkpoint=None,
-                      stream=None) -> LayerNormOut:
+@_on_device
+def layernorm_forward(x, gain, bias=None, *, eps=1e-5, x_checkpoint=None, y_checkpoint=None) -> LayerNormOut:
     """``y = (x - mean) * rstd * gain + bias`` over the columns of ``x``.
 
     gain, bias: [cols], of one dtype (that of x or the other).  mean and rstd
@@ -222,14 +244,14 @@ def layernorm_forward(x, gain, bias=None, *, eps=1e-5, x_checkpoint=None, y_chec
     pdt = dtype_code(gain.dtype)
     if bias is not None:
         _check_vector("bias", bias, cols, dev, gain.dtype)
-    with _scope(stream, dev):
-        xc = _as_checkpoint("x_checkpoint", x_checkpoint, (tokens, cols), dev)
-        yc = _as_checkpoint("y_checkpoint", y_checkpoint, (tokens, cols), dev)
-        y = torch.empty(tokens, cols, dtype=x.dtype, device=dev)
-        mean, rstd = torch.empty(2, tokens, dtype=torch.float32, device=dev).unbind(0)
-        st = _lib.lib().muon_layernorm_forward(
-            x.data_ptr(), ld, gain.data_ptr(), _ptr(bias), tokens, cols, dt, pdt, float(eps),
-            y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ref(xc), _ref(yc), _stream_of(dev))
+    xc = _as_checkpoint("x_checkpoint", x_checkpoint, (tokens, cols), dev)
+    yc = _as_checkpoint("y_checkpoint", y_checkpoint, (tokens, cols), dev)
+    y = torch.empty((tokens, cols), dtype=x.dtype, device=dev)
+    mean = torch.empty(tokens, dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
+    st = _lib.lib().muon_layernorm_forward(
+        x.data_ptr(), ld, gain.data_ptr(), _ptr(bias), tokens, cols, dt, pdt, float(eps),
+        y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ref(xc), _ref(yc), _raw_stream(dev.index))
     _check(st, "muon_layernorm_forward")
     return LayerNormOut(y, mean, rstd, xc, yc)
 
@@ -238,8 +260,9 @@ def layernorm_workspace_bytes(tokens: int, cols: int) -> int:
     return int(_lib.lib().muon_layernorm_workspace_bytes(tokens, cols))
 
 
+@_on_device
 def layernorm_backward(dy, x, gain, mean, rstd, *, bias=True, dgain=None, dbias=None,
-                       accumulate=False, workspace=None, stream=None):
+                       accumulate=False, workspace=None):
     """``(dx, dgain, dbias)`` of :func:`layernorm_forward`.
 
     x: the forward's input, or an ActCheckpoint of it.  dgain and dbias have
@@ -266,18 +289,17 @@ def layernorm_backward(dy, x, gain, mean, rstd, *, bias=True, dgain=None, dbias=
             _check_vector(name, t, cols, dev, gain.dtype)
         elif accumulate and wanted:
             raise ValueError(f"accumulate needs {name}")
-    with _scope(stream, dev):
-        dx = torch.empty(tokens, cols, dtype=dy.dtype, device=dev)
-        if dgain is None:
-            dgain = torch.empty_like(gain)
-        if bias and dbias is None:
-            dbias = torch.empty_like(gain)
-        ws = _workspace(layernorm_workspace_bytes(tokens, cols), dev, workspace)
-        st = _lib.lib().muon_layernorm_backward(
-            dy.data_ptr(), ldy, None if ck is not None else x.data_ptr(), ldx, _ref(ck),
-            gain.data_ptr(), mean.data_ptr(), rstd.data_ptr(), tokens, cols, dt, pdt,
-            dx.data_ptr(), dgain.data_ptr(), _ptr(dbias), int(accumulate), ws.data_ptr(),
-            ws.numel() * ws.element_size(), _stream_of(dev))
+    dx = torch.empty(tokens, cols, dtype=dy.dtype, device=dev)
+    if dgain is None:
+        dgain = torch.empty_like(gain)
+    if bias and dbias is None:
+        dbias = torch.empty_like(gain)
+    ws = _workspace(layernorm_workspace_bytes(tokens, cols), dev, workspace)
+    st = _lib.lib().muon_layernorm_backward(
+        dy.data_ptr(), ldy, None if ck is not None else x.data_ptr(), ldx, _ref(ck),
+        gain.data_ptr(), mean.data_ptr(), rstd.data_ptr(), tokens, cols, dt, pdt,
+        dx.data_ptr(), dgain.data_ptr(), _ptr(dbias), int(accumulate), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _raw_stream(dev.index))
     _check(st, "muon_layernorm_backward")
     return dx, dgain, dbias
 
@@ -288,8 +310,8 @@ def weight_grad_workspace_bytes(count: int, tokens: int, rows: int, cols: int,
                                                            dtype_code(dtype)))
 
 
-def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, workspace=None,
-                stream=None):
+@_on_device
+def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, workspace=None):
     """Gradient of the weight of ``y = x W^T`` from ``dy`` [tokens, rows] and
     the checkpoint of ``x`` [tokens, cols]: ``G = dy^T x`` [rows, cols].
 
@@ -327,15 +349,14 @@ def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, w
         if dtype is not None and G.dtype != dtype:
             raise TypeError(f"G has dtype {G.dtype}, expected {dtype}")
     gdt = dtype_code(G.dtype if G is not None else dtype or dy.dtype)
-    with _scope(stream, dev):
-        if G is None:
-            G = torch.empty(shape, dtype=dtype or dy.dtype, device=dev)
-        if count == 0:
-            return G
-        ws = _workspace(weight_grad_workspace_bytes(count, tokens, rows, ck.cols, dy.dtype), dev,
-                        workspace)
-        st = _lib.lib().muon_weight_grad(
-            dy.data_ptr(), ld, dt, _ref(ck), _ptr(offsets), count, rows, G.data_ptr(), gdt,
-            int(accumulate), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev))
+    if G is None:
+        G = torch.empty(shape, dtype=dtype or dy.dtype, device=dev)
+    if count == 0:
+        return G
+    ws = _workspace(weight_grad_workspace_bytes(count, tokens, rows, ck.cols, dy.dtype), dev,
+                    workspace)
+    st = _lib.lib().muon_weight_grad(
+        dy.data_ptr(), ld, dt, _ref(ck), _ptr(offsets), count, rows, G.data_ptr(), gdt,
+        int(accumulate), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dev.index))
     _check(st, "muon_weight_grad")
     return G
