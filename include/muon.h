@@ -299,8 +299,9 @@ int muon_adamw_step_grouped(const muon_adamw_tensor* tensors, int64_t count, int
  *  Stream, workspace, errors  as for the Muon entry points: everything that
  *           the host can see is validated before anything is enqueued, no
  *           allocation, no synchronisation; calls that overlap in time need
- *           workspaces of their own.  Results are the same bits on every run:
- *           all sums have a fixed order.
+ *           workspaces of their own.  A workspace of 0 bytes may be NULL.
+ *           Results are the same bits on every run: all sums have a fixed
+ *           order.
  */
 #define MUON_MAX_TOKENS (((int64_t)1) << 30)
 #define MUON_CKPT_BLOCK 32
@@ -365,8 +366,8 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
  * parts, which hold its 24 bits) and accumulate in float32; G is rounded once.
  */
 #define MUON_WEIGHT_GRAD_MAX_COUNT (1 << 20)
-size_t muon_weight_grad_workspace_bytes(int64_t count, int64_t tokens, int64_t rows, int64_t cols,
-                                        int dtype);
+size_t muon_weight_grad_workspace_bytes(int64_t count, int with_offsets, int64_t tokens,
+                                        int64_t rows, int64_t cols, int dtype);
 int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x,
                      const int64_t* offsets, int64_t count, int64_t rows, void* G, int g_dtype,
                      int accumulate, void* workspace, size_t workspace_bytes, void* stream);

@@ -160,7 +160,7 @@ def lib():
     L.muon_layernorm_backward.argtypes = [p, i64, p, i64, ck, p, p, p, i64, i64, i32, i32,
                                           p, p, p, i32, p, ctypes.c_size_t, p]
     L.muon_layernorm_backward.restype = i32
-    L.muon_weight_grad_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
+    L.muon_weight_grad_workspace_bytes.argtypes = [i64, i32, i64, i64, i64, i32]
     L.muon_weight_grad_workspace_bytes.restype = ctypes.c_size_t
     L.muon_weight_grad.argtypes = [p, i64, i32, ck, p, i64, i64, p, i32, i32, p,
                                    ctypes.c_size_t, p]

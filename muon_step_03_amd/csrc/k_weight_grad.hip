@@ -445,30 +445,23 @@ __device__ __forceinline__ bf16x8_t frag_x(const LDS_AS char* tile, int kb, int 
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// Sixteen checkpoint bytes -> sixteen bf16, exact; a marked block gives NaN.
+// Four checkpoint bytes -> four bf16, exact; a marked block gives NaN.
 template <int FMT>
-__device__ __forceinline__ void unpack16(u32x4_t q, int byte, uint32_t (&o)[8]) {
+__device__ __forceinline__ void unpack4(uint32_t q, int byte, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == MUON_CKPT_E4M3) {
     // the conversion scales by the exponent of `up`, 255 giving NaN
     const float up = __uint_as_float(uint32_t(byte) << 23);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], up, false));
-      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[i], up, true));
-    }
+    lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, up, false));
+    hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, up, true));
   } else {
     // bytes offset to unsigned, the offset taken off again in the scaling
     const float up = ckpt_up(byte), off = -128.f * up;
+    const uint32_t w = q ^ 0x80808080u;
+    float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = q[i] ^ 0x80808080u;
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = __builtin_fmaf(float((w >> (8 * j)) & 0xffu), up, off);
-      o[2 * i] = f2bf2(v[0], v[1]);
-      o[2 * i + 1] = f2bf2(v[2], v[3]);
-    }
+    for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(float((w >> (8 * j)) & 0xffu), up, off);
+    lo = f2bf2(v[0], v[1]);
+    hi = f2bf2(v[2], v[3]);
   }
 }
 
@@ -549,7 +542,13 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
     sw = *reinterpret_cast<const LDS_AS uint32_t*>(smem + at + C::Q_BYTES + wave * 256 + lane * 4);
   };
   uint32_t o[8];
-  auto unpack = [&]() { unpack16<FMT>(q, (sw >> (8 * ((x_c / 2) & 3))) & 0xff, o); };
+  auto unpack = [&](int i) {
+    unpack4<FMT>(q[i], (sw >> (8 * ((x_c / 2) & 3))) & 0xff, o[2 * i], o[2 * i + 1]);
+  };
+  auto unpack_all = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack(i);
+  };
   auto write_x = [&](auto tile_x) {
     LDS_AS char* x = smem + C::X_AT + decltype(tile_x)::value * C::X_BYTES;
     *reinterpret_cast<LDS_AS u32x4_t*>(x + x_at<BN>(x_k, 2 * x_c)) = u32x4_t{o[0], o[1], o[2], o[3]};
@@ -632,12 +631,15 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
     if (more_y) issue_y(buf_3, end, 0, k + 3);
     multiply(0, 1);
     if (more_y) issue_y(buf_3, end, 1, k + 3);
+    if (more_x) unpack(0);
     multiply(0, 2);
     if (more_q) issue_q(end, SLOT, k + 4);
+    if (more_x) unpack(1);
     multiply(0, 3);
     if (more_q) issue_s(end, SLOT, k + 4);
+    if (more_x) unpack(2);
     multiply(1, 0);
-    if (more_x) unpack();
+    if (more_x) unpack(3);
     multiply(1, 1);
     if (more_x) write_x(tile_2);
     multiply(1, 2);
@@ -678,11 +680,11 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
       wait_vmcnt<0>();
     asm volatile("" ::: "memory");
     read_q(Q0);
-    unpack();
+    unpack_all();
     write_x(c0);
     if (1 < steps) {
       read_q(Q1);
-      unpack();
+      unpack_all();
       write_x(c1);
     }
     if (steps <= PARTS && last < BK) zero_tail(c0);
@@ -745,33 +747,52 @@ __global__ __launch_bounds__(kThreads) void repack_kernel(const void* dy, int64_
 }
 
 // Adds the partial sums of the matrices with several pieces, in their order:
-// kJoin elements at a time.
-constexpr int kJoin = 8 * kThreads;
+// kJoin elements at a time, four per thread, the loads of eight pieces in
+// flight.
+constexpr int kJoin = 4 * kThreads;
 __global__ __launch_bounds__(kThreads) void join_kernel(const WeightGrad p, int64_t blocks) {
   const int64_t size = int64_t(p.rows) * p.cols;
   const Split* splits = reinterpret_cast<const Split*>(static_cast<const Piece*>(p.table) + p.pieces);
   const int64_t work = p.offsets ? splits[p.count].e * blocks : blocks;
   for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-    const int64_t which = i / blocks, at = (i - which * blocks) * kJoin + threadIdx.x * 8;
+    const int64_t which = i / blocks, at = (i - which * blocks) * kJoin + threadIdx.x * 4;
     const Split sp = p.offsets ? splits[which] : Split{0, int(p.pieces), 0};
     if (at >= size) continue;
-    const int left = size - at < 8 ? int(size - at) : 8;
-    float v[8] = {};
-#pragma unroll 2
-    for (int j = 0; j < sp.parts; ++j) {
-      const float* part = p.partial + (sp.slot + j) * size + at;
-      float w[8];
-      load_vec<false>(part, 0, left, w);
-      load_vec<false>(part, 4, left, w + 4);
+    const int left = size - at < 4 ? int(size - at) : 4;
+    const float* part = p.partial + sp.slot * size + at;
+    float v[4] = {};
+    if (left == 4) {
+#pragma unroll 8
+      for (int j = 0; j < sp.parts; ++j) {
+        const u32x4_a4 w = *reinterpret_cast<const u32x4_a4*>(part + j * size);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] += w[c];
+        for (int c = 0; c < 4; ++c) v[c] += __uint_as_float(w[c]);
+      }
+    } else {
+      for (int j = 0; j < sp.parts; ++j)
+        for (int c = 0; c < 4; ++c) v[c] += c < left ? part[j * size + c] : 0.f;
     }
-    // the matrix as one row
-    WeightGrad flat = p;
-    flat.rows = 1;
-    flat.cols = left;
-    store_row8(flat, nullptr, sp.e * size + at, 0, 0, f32x4_t{v[0], v[1], v[2], v[3]},
-               f32x4_t{v[4], v[5], v[6], v[7]});
+    const int64_t to = sp.e * size + at;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c >= left) break;
+      if (p.g_bf16) {
+        const uint16_t* g = static_cast<const uint16_t*>(p.G) + to + c;
+        if (p.accumulate) v[c] += bf2f(*g);
+      } else {
+        if (p.accumulate) v[c] += static_cast<const float*>(p.G)[to + c];
+      }
+    }
+    if (p.g_bf16) {
+      uint16_t* g = static_cast<uint16_t*>(p.G) + to;
+      typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+      if (left == 4)
+        *reinterpret_cast<u32x2_a2*>(g) = u32x2_a2{f2bf2(v[0], v[1]), f2bf2(v[2], v[3])};
+      else
+        for (int c = 0; c < left; ++c) g[c] = f2bf(v[c]);
+    } else {
+      store_vec<false>(static_cast<float*>(p.G) + to, 0, left, v);
+    }
   }
 }
 
@@ -780,17 +801,21 @@ int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 // Parts that a matrix of `tokens` is cut into, `count` matrices at once: the
 // estimate below at its least.  In microseconds, measured on one MI355X: a
-// round of blocks (one per CU) takes 6 (start, first loads, stores) and 0.95
-// for each step of 32 tokens; the join takes 4 and, through the Infinity Cache,
-// moves 8 bytes per element and part at 10 TB/s.  4096 x 1024 over 16384 tokens, 64 tiles: 182 us in 2
-// parts, 131 in 4, 151 in 8.
-int64_t parts_of(int64_t count, int64_t tokens, int64_t rows, int64_t cols, int64_t tiles) {
-  const double steps = double(cdiv(tokens, BK)), g = double(count) * double(rows) * double(cols);
+// round of blocks (one per CU) takes 6 (start, first loads, stores) and 0.6
+// for each step on a quarter of the CUs, 0.95 on all of them; the join takes
+// 4 and, through the Infinity Cache, moves 8 bytes per element and part at
+// 10 TB/s.  4096 x 1024 over 16384 tokens, 64 tiles: 182 us in 2 parts, 131 in 4,
+// 151 in 8.  `steps_of`: steps of 32 tokens (three for float32 dy).
+int64_t parts_of(int64_t count, int64_t tokens, int64_t rows, int64_t cols, int64_t tiles,
+                 int steps_of) {
+  const double steps = double(cdiv(tokens, BK) * steps_of);
+  const double g = double(count) * double(rows) * double(cols);
   int64_t best = 1;
   double least = 0;
   for (int64_t n = 1; n <= 64 && n <= cdiv(tokens, 4 * BK); ++n) {
-    const double rounds = double(cdiv(count * tiles * n, 256));
-    const double us = rounds * (6 + 0.95 * steps / double(n)) + (n > 1 ? 4 + g * double(n) * 8 / 1e7 : 0);
+    const double blocks = double(count * tiles * n), rounds = double(cdiv(count * tiles * n, 256));
+    const double step = 0.48 + 0.47 * std::min(1.0, blocks / 256);
+    const double us = rounds * (6 + step * steps / double(n)) + (n > 1 ? 4 + g * double(n) * 8 / 1e7 : 0);
     if (n == 1 || us < least) {
       best = n;
       least = us;
@@ -819,7 +844,7 @@ WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int
   if (w.wide && !(bf16 && rows % 8 == 0))
     w.repack_bytes = size_t(tokens) * size_t(cdiv(rows, 8) * 8) * (bf16 ? 2 : 6);
   const int64_t even = cdiv(tokens, count);
-  int64_t chunk = cdiv(even, parts_of(count, even, rows, cols, tiles));
+  int64_t chunk = cdiv(even, parts_of(count, even, rows, cols, tiles, bf16 ? 1 : 3));
   if (ragged) chunk = std::max(chunk, tokens / 256 * tiles);
   chunk = std::max<int64_t>(4 * BK, cdiv(std::min(chunk, MUON_MAX_TOKENS), BK) * BK);
   w.chunk = uint32_t(chunk);

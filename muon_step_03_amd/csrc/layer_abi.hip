@@ -97,11 +97,10 @@ int launched(hipError_t e, const char* what, hipStream_t s) {
 
 size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
-// Workspace of a weight gradient (0: the sizes cannot be launched).
+// Workspace of a weight gradient.
 size_t weight_grad_bytes(const WeightGradPlan& plan) {
-  return plan.pieces > 0 ? align_up(plan.partial_bytes) + align_up(plan.table_bytes) +
-                               plan.repack_bytes + kAlign
-                         : 0;
+  const size_t n = align_up(plan.partial_bytes) + align_up(plan.table_bytes) + plan.repack_bytes;
+  return plan.pieces > 0 && n > 0 ? n + kAlign : 0;
 }
 
 char* align_ptr(void* p) {
@@ -198,7 +197,8 @@ int muon_layernorm_forward(const void* x, int64_t ldx, const void* gain, const v
 
 size_t muon_layernorm_workspace_bytes(int64_t tokens, int64_t cols) {
   if (!sizes_ok(tokens, cols)) return 0;
-  return size_t(ln_backward_blocks(tokens, cols)) * 2 * size_t(cols) * 4 + kAlign;
+  const int blocks = ln_backward_blocks(tokens, cols);
+  return blocks > 1 ? size_t(blocks) * 2 * size_t(cols) * 4 + kAlign : 0;
 }
 
 int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
@@ -211,7 +211,7 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
   if (x_ckpt)
     if (const int st = check_ckpt(x_ckpt, tokens, cols); st != MUON_OK) return st;
   const size_t es = elem_size(dtype), ps = elem_size(param_dtype);
-  if (!gain || !dgain || !workspace || (x && x_ckpt)) return MUON_ERR_INVALID_ARGUMENT;
+  if (!gain || !dgain || (x && x_ckpt)) return MUON_ERR_INVALID_ARGUMENT;
   if (tokens > 0) {
     if (!dy || !dx || !mean || !rstd || (!x && !x_ckpt)) return MUON_ERR_INVALID_ARGUMENT;
     if (!stride_ok(lddy, cols) || (x && !stride_ok(ldx, cols))) return MUON_ERR_INVALID_ARGUMENT;
@@ -231,8 +231,9 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
   b.add(dbias, size_t(cols) * ps, true);
   b.add(workspace, workspace_bytes, true);
   if (b.clash()) return MUON_ERR_INVALID_ARGUMENT;
-  if (workspace_bytes < muon_layernorm_workspace_bytes(tokens, cols))
-    return MUON_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = muon_layernorm_workspace_bytes(tokens, cols);
+  if (need > 0 && !workspace) return MUON_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < need) return MUON_ERR_WORKSPACE_TOO_SMALL;
   if (tokens == 0 && accumulate) return MUON_OK;
   LnBackward p{};
   p.dy = dy;
@@ -261,12 +262,12 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
   return launched(launch_ln_params(p, s), "layernorm_params", s);
 }
 
-size_t muon_weight_grad_workspace_bytes(int64_t count, int64_t tokens, int64_t rows, int64_t cols,
-                                        int dtype) {
+size_t muon_weight_grad_workspace_bytes(int64_t count, int with_offsets, int64_t tokens,
+                                        int64_t rows, int64_t cols, int dtype) {
   if (!dtype_ok(dtype) || count < 1 || count > MUON_WEIGHT_GRAD_MAX_COUNT || !sizes_ok(tokens, cols) || rows < 1 || rows > MUON_MAX_DIM)
     return 0;
   return weight_grad_bytes(
-      weight_grad_plan(count, tokens, rows, cols, true, dtype == MUON_DTYPE_BF16));
+      weight_grad_plan(count, tokens, rows, cols, with_offsets != 0, dtype == MUON_DTYPE_BF16));
 }
 
 int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x,
@@ -280,7 +281,7 @@ int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x
   if (count == 0) return MUON_OK;
   if (!offsets && count != 1) return MUON_ERR_INVALID_ARGUMENT;
   const size_t es = elem_size(dtype), gs = elem_size(g_dtype);
-  if (!G || !aligned(G, gs) || !aligned(offsets, 8) || !aligned(dy, es) || !workspace)
+  if (!G || !aligned(G, gs) || !aligned(offsets, 8) || !aligned(dy, es))
     return MUON_ERR_INVALID_ARGUMENT;
   if (tokens > 0 && (!dy || !stride_ok(lddy, rows))) return MUON_ERR_INVALID_ARGUMENT;
   size_t g_bytes;
@@ -296,7 +297,9 @@ int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x
   const WeightGradPlan plan = weight_grad_plan(count, tokens, rows, cols, offsets != nullptr,
                                                dtype == MUON_DTYPE_BF16);
   if (plan.pieces <= 0) return MUON_ERR_INVALID_SHAPE;
-  if (workspace_bytes < weight_grad_bytes(plan)) return MUON_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = weight_grad_bytes(plan);
+  if (need > 0 && !workspace) return MUON_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < need) return MUON_ERR_WORKSPACE_TOO_SMALL;
   if (tokens == 0 && accumulate) return MUON_OK;
   WeightGrad p{};
   p.dy = dy;

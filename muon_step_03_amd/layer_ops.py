@@ -87,14 +87,18 @@ def _check_vector(name, t, n, device, dtype=None):
 
 
 def _workspace(need, device, workspace):
+    """(tensor, address, bytes) of a workspace of at least ``need`` bytes."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {device}")
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, "
                          f"{need} needed")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 class ActCheckpoint:
@@ -294,20 +298,21 @@ def layernorm_backward(dy, x, gain, mean, rstd, *, bias=True, dgain=None, dbias=
         dgain = torch.empty_like(gain)
     if bias and dbias is None:
         dbias = torch.empty_like(gain)
-    ws = _workspace(layernorm_workspace_bytes(tokens, cols), dev, workspace)
+    _ws, at, size = _workspace(layernorm_workspace_bytes(tokens, cols), dev, workspace)
     st = _lib.lib().muon_layernorm_backward(
         dy.data_ptr(), ldy, None if ck is not None else x.data_ptr(), ldx, _ref(ck),
         gain.data_ptr(), mean.data_ptr(), rstd.data_ptr(), tokens, cols, dt, pdt,
-        dx.data_ptr(), dgain.data_ptr(), _ptr(dbias), int(accumulate), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _raw_stream(dev.index))
+        dx.data_ptr(), dgain.data_ptr(), _ptr(dbias), int(accumulate), at, size,
+        _raw_stream(dev.index))
     _check(st, "muon_layernorm_backward")
     return dx, dgain, dbias
 
 
-def weight_grad_workspace_bytes(count: int, tokens: int, rows: int, cols: int,
+def weight_grad_workspace_bytes(count: int, with_offsets: bool, tokens: int, rows: int, cols: int,
                                 dtype: torch.dtype) -> int:
-    return int(_lib.lib().muon_weight_grad_workspace_bytes(count, tokens, rows, cols,
-                                                           dtype_code(dtype)))
+    """Workspace of :func:`weight_grad`; dtype: that of dy."""
+    return int(_lib.lib().muon_weight_grad_workspace_bytes(count, int(with_offsets), tokens, rows,
+                                                           cols, dtype_code(dtype)))
 
 
 @_on_device
@@ -353,10 +358,10 @@ def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, w
         G = torch.empty(shape, dtype=dtype or dy.dtype, device=dev)
     if count == 0:
         return G
-    ws = _workspace(weight_grad_workspace_bytes(count, tokens, rows, ck.cols, dy.dtype), dev,
-                    workspace)
+    need = weight_grad_workspace_bytes(count, offsets is not None, tokens, rows, ck.cols, dy.dtype)
+    _ws, at, size = _workspace(need, dev, workspace)
     st = _lib.lib().muon_weight_grad(
         dy.data_ptr(), ld, dt, _ref(ck), _ptr(offsets), count, rows, G.data_ptr(), gdt,
-        int(accumulate), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dev.index))
+        int(accumulate), at, size, _raw_stream(dev.index))
     _check(st, "muon_weight_grad")
     return G

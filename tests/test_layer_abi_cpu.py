@@ -100,7 +100,7 @@ def test_forward_no_tokens(L):
 
 
 def backward(L, dy=A[0], lddy=64, x=A[1], ldx=64, xc=None, gain=A[2], mean=A[3], rstd=A[4],
-             tokens=16, cols=64, dtype=F32, pdtype=F32, dx=A[5], dgain=A[6], dbias=A[7], acc=0,
+             tokens=1000, cols=64, dtype=F32, pdtype=F32, dx=A[5], dgain=A[6], dbias=A[7], acc=0,
              ws=A[10], wsb=1 << 20):
     return L.muon_layernorm_backward(dy, lddy, x, ldx, xc, gain, mean, rstd, tokens, cols, dtype,
                                      pdtype, dx, dgain, dbias, acc, ws, wsb, None)
@@ -112,16 +112,16 @@ def backward(L, dy=A[0], lddy=64, x=A[1], ldx=64, xc=None, gain=A[2], mean=A[3],
     (dict(mean=None), ARG), (dict(rstd=None), ARG), (dict(dx=None), ARG), (dict(dgain=None), ARG),
     (dict(lddy=63), ARG), (dict(ldx=0), ARG), (dict(ws=None), ARG), (dict(wsb=16), WS),
     (dict(dx=A[0]), ARG), (dict(dx=A[1] + 8), ARG), (dict(dgain=A[7]), ARG),
-    (dict(dbias=A[2] + 4), ARG), (dict(ws=A[5] - 16), ARG), (dict(dx=A[5] + 2), ARG),
+    (dict(dbias=A[2] + 4), ARG), (dict(ws=A[5] - 16), ARG), (dict(ws=A[0], tokens=16), ARG), (dict(dx=A[5] + 2), ARG),
 ])
 def test_backward_refusals(L, kw, status):
     assert backward(L, **kw) == status
 
 
 def test_backward_source_is_one_of_two(L):
-    assert backward(L, xc=ckpt()) == ARG            # both
+    assert backward(L, xc=ckpt(tokens=1000)) == ARG            # both
     assert backward(L, x=None, xc=ckpt(cols=32)) == SHAPE
-    assert backward(L, x=None, xc=ckpt(), dx=A[9]) == ARG
+    assert backward(L, x=None, xc=ckpt(tokens=1000), dx=A[9]) == ARG
 
 
 def test_backward_no_tokens_accumulating(L):
@@ -130,7 +130,8 @@ def test_backward_no_tokens_accumulating(L):
 
 def weight(L, dy=A[0], lddy=96, dtype=F32, x=None, offsets=None, count=1, rows=96, G=A[2],
            gdtype=F32, acc=0, ws=A[4], wsb=1 << 26):
-    return L.muon_weight_grad(dy, lddy, dtype, x if x is not None else ckpt(), offsets, count,
+    x = x if x is not None else ckpt(tokens=4000)
+    return L.muon_weight_grad(dy, lddy, dtype, x, offsets, count,
                               rows, G, gdtype, acc, ws, wsb, None)
 
 
@@ -160,23 +161,26 @@ def test_weight_grad_nothing_to_do(L):
 def test_workspace_sizes(L):
     assert L.muon_layernorm_workspace_bytes(-1, 5) == 0
     assert L.muon_layernorm_workspace_bytes(5, 0) == 0
-    assert L.muon_layernorm_workspace_bytes(0, 64) == 256
+    # one block's rows need no partial sums
+    assert L.muon_layernorm_workspace_bytes(0, 64) == 0
+    assert L.muon_layernorm_workspace_bytes(12, 768) == 0
     # partial sums grow with the tokens up to a fixed number of blocks
     big = L.muon_layernorm_workspace_bytes(1 << 20, 1024)
     assert big == L.muon_layernorm_workspace_bytes(1 << 30, 1024) > 1024 * 8
-    assert L.muon_weight_grad_workspace_bytes(0, 5, 5, 5, 0) == 0
-    assert L.muon_weight_grad_workspace_bytes(1, 5, 0, 5, 0) == 0
-    assert L.muon_weight_grad_workspace_bytes(1, -1, 5, 5, 0) == 0
-    assert L.muon_weight_grad_workspace_bytes(1, 5, 5, _lib.MUON_MAX_DIM + 1, 0) == 0
-    assert L.muon_weight_grad_workspace_bytes(1, 0, 5, 5, 0) >= 256
-    assert L.muon_weight_grad_workspace_bytes(1, 5, 5, 5, 2) == 0
+    assert L.muon_weight_grad_workspace_bytes(0, 0, 5, 5, 5, 0) == 0
+    assert L.muon_weight_grad_workspace_bytes(1, 0, 5, 0, 5, 0) == 0
+    assert L.muon_weight_grad_workspace_bytes(1, 0, -1, 5, 5, 0) == 0
+    assert L.muon_weight_grad_workspace_bytes(1, 0, 5, 5, _lib.MUON_MAX_DIM + 1, 0) == 0
+    assert L.muon_weight_grad_workspace_bytes(1, 0, 5, 5, 5, 2) == 0
+    # one piece, nothing to repack
+    assert L.muon_weight_grad_workspace_bytes(1, 0, 96, 768, 768, BF16) == 0
     # partial sums and a table entry for each piece of at least 128 tokens,
     # and dy once more in three bf16 parts (float32) or in padded rows
     for count, tokens, rows, cols in [(1, 1 << 20, 64, 64), (64, 49152, 1408, 512),
                                       (1, 16384, 4096, 1024), (7, 100, 33, 1000),
                                       (1, 65536, 1001, 777)]:
         for dtype, part in ((F32, 6), (BF16, 0 if rows % 8 == 0 else 2)):
-            got = L.muon_weight_grad_workspace_bytes(count, tokens, rows, cols, dtype)
+            got = L.muon_weight_grad_workspace_bytes(count, 1, tokens, rows, cols, dtype)
             pieces = tokens // 128 + count
             most = pieces * (rows * cols * 4 + 48) + (rows + 7) * tokens * part + 1024
             assert 256 <= got <= most

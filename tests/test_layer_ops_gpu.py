@@ -374,7 +374,7 @@ def test_same_bits_every_time_and_given_buffers():
     first = M.layernorm_backward(dy, x, gain, out.mean, out.rstd)
     G = M.weight_grad(dy, out.y_checkpoint)
     ws = torch.full((max(M.layernorm_workspace_bytes(3000, 520),
-                         M.weight_grad_workspace_bytes(1, 3000, 520, 520, BF16)),), 255,
+                         M.weight_grad_workspace_bytes(1, False, 3000, 520, 520, BF16)),), 255,
                     dtype=torch.uint8, device=DEV)
     for _ in range(3):
         again = M.layernorm_backward(dy, x, gain, out.mean, out.rstd, workspace=ws)
@@ -454,7 +454,8 @@ def test_captured_run():
     (lambda x, v, ck: M.layernorm_backward(x, ck, v, x[:, 0], x[:, 0]), ValueError, "contiguous"),
     (lambda x, v, ck: M.layernorm_backward(x, ck, v, v[:8], v[:8], accumulate=True), ValueError, "needs dgain"),
     (lambda x, v, ck: M.layernorm_backward(x, ck, v, v[:8], v[:8], bias=False, dbias=v), ValueError, "bias=False"),
-    (lambda x, v, ck: M.layernorm_backward(x, ck, v, v[:8], v[:8], workspace=v[:4]), ValueError, "workspace holds"),
+    (lambda x, v, ck: M.weight_grad(x, ck, offsets=torch.zeros(3, dtype=torch.int64, device=DEV), workspace=v[:4]),
+     ValueError, "workspace holds"),
     (lambda x, v, ck: M.checkpoint_restore(ck, torch.float16), TypeError, "float32 or bfloat16"),
     (lambda x, v, ck: M.checkpoint_restore(ck, out=x.t()), ValueError, "shape"),
     (lambda x, v, ck: M.weight_grad(x[:7], ck), ValueError, "expected 7 x 64"),
