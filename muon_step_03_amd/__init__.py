@@ -16,3 +16,4 @@ from .layer_ops import (  # noqa: F401
     ActCheckpoint, LayerNormOut, checkpoint_restore, checkpoint_save, layernorm_backward,
     layernorm_forward, layernorm_workspace_bytes, weight_grad, weight_grad_workspace_bytes,
 )
+from .layers import layer_norm, linear  # noqa: F401

@@ -400,6 +400,22 @@ class MuonStep:
         return groups, keep
 
     @torch.no_grad()
+    def accumulate_grad(self, index, dy, checkpoint):
+        """Adds the gradient of parameter ``index``, the weight of
+        ``y = x W^T``, to its ``.grad``: from ``dy`` [tokens, rows] and the
+        checkpoint of ``x`` (an ``ActCheckpoint``), one micro-batch per call.
+        The first call of a step (``.grad`` is None) writes it."""
+        from .layer_ops import weight_grad
+        p = self.params[index]
+        if dy.ndim != 2 or (dy.shape[1], checkpoint.cols) != tuple(p.shape):
+            raise ValueError(f"dy {tuple(dy.shape)} and x {checkpoint.shape} do not make the "
+                             f"gradient of a parameter of shape {tuple(p.shape)}")
+        if p.grad is None:
+            p.grad = weight_grad(dy, checkpoint, dtype=p.dtype)
+        else:
+            weight_grad(dy, checkpoint, G=p.grad, accumulate=True)
+
+    @torch.no_grad()
     def step(self, stats=None):
         """One step of every parameter.  ``stats``: optional float32 GPU
         tensor of ``len(params) * MUON_STATS_PER_MATRIX`` floats, rows in

@@ -186,6 +186,20 @@ def test_workspace_sizes(L):
             assert 256 <= got <= most
 
 
+def test_layers_refuse_mismatched_arguments():
+    x, W = torch.zeros(4, 64), torch.zeros(8, 64)
+    with pytest.raises(ValueError, match="2-D"):
+        M.linear(x, W[0])
+    with pytest.raises(TypeError, match="dtype"):
+        M.linear(x, W.bfloat16())
+    with pytest.raises(ValueError, match="columns"):
+        M.linear(x, W[:, :32])
+    with pytest.raises(ValueError, match="on a GPU"):
+        M.linear(x, W.clone().requires_grad_())
+    with pytest.raises(ValueError, match="on a GPU"):
+        M.layer_norm(x, W[0])
+
+
 def test_binding_refuses_what_is_not_on_a_gpu():
     x = torch.zeros(4, 64)
     v = torch.zeros(64)
