@@ -16,7 +16,6 @@ uses tensors across streams orders them, as with any PyTorch operator.
 from __future__ import annotations
 
 import ctypes
-import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -30,24 +29,26 @@ _FORMAT_NAMES = {v: k for k, v in FORMATS.items()}
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle, no object
+_current_device = torch._C._cuda_getDevice
 
 
-def _on_device(fn):
-    """Runs ``fn(x, ...)`` with the device of its first argument (a tensor or
-    an ActCheckpoint) current, on the stream given as ``stream``."""
-    @functools.wraps(fn)
-    def call(x, *args, stream=None, **kw):
-        device = getattr(x, "device", None)
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            with torch.cuda.stream(stream):
-                return fn(x, *args, **kw)
-        if device is not None and device.type == "cuda" and device.index != torch.cuda.current_device():
-            with torch.cuda.device(device):
-                return fn(x, *args, **kw)
-        return fn(x, *args, **kw)
-    return call
+def _away(t, stream) -> bool:
+    """Whether a call on ``t`` has to change the current device or stream."""
+    if stream is not None:
+        return True
+    device = getattr(t, "device", None)
+    return device is not None and device.type == "cuda" and device.index != _current_device()
+
+
+def _there(fn, t, stream, *args, **kw):
+    """``fn(t, ...)`` with the device of ``t``, and ``stream`` if given, current."""
+    if stream is None:
+        with torch.cuda.device(t.device):
+            return fn(t, *args, **kw)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.stream(stream):
+        return fn(t, *args, **kw)
 
 
 def _check_rows(name, t, device=None, shape=None, dtype=None, contiguous=False):
@@ -107,7 +108,7 @@ class ActCheckpoint:
     float8_e4m3fn or int8, ``scale`` uint8 [tokens, blocks of 32 columns up to
     a multiple of 4].  An element stands for ``q * 2^(scale - 127)``."""
 
-    __slots__ = ("_q", "_scale", "_cols", "_code")
+    __slots__ = ("_q", "_scale", "_buffer", "_shape", "_store", "_c")
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor, cols: int):
         if q.dtype not in _FORMAT_CODES:
@@ -122,7 +123,9 @@ class ActCheckpoint:
                                  f"{(tokens, pitch)} for {cols} columns, got {tuple(t.shape)}")
         if scale.device != q.device:
             raise ValueError(f"scale is on {scale.device}, q on {q.device}")
-        self._q, self._scale, self._cols, self._code = q, scale, cols, _FORMAT_CODES[q.dtype]
+        self._q, self._scale, self._buffer = q, scale, None
+        self._shape, self._store = (tokens, cols), q.dtype
+        self._c = None
 
     @classmethod
     def empty(cls, tokens: int, cols: int, fmt: str = "e4m3", device="cuda") -> "ActCheckpoint":
@@ -132,40 +135,54 @@ class ActCheckpoint:
         except KeyError:
             raise ValueError(f"unknown checkpoint format {fmt!r}; expected one of "
                              f"{sorted(FORMATS)}") from None
+        # one buffer of its own for both; the views are made when asked for
+        size = tokens * ((cols + 31) // 32 * 32)
         ck = cls.__new__(cls)
-        ck._q = torch.empty((tokens, _lib.ckpt_q_pitch(cols)), dtype=store, device=device)
-        ck._scale = torch.empty((tokens, _lib.ckpt_scale_pitch(cols)), dtype=torch.uint8,
-                                device=device)
-        ck._cols, ck._code = cols, _FORMAT_CODES[store]
+        ck._buffer = torch.empty(size + tokens * ((cols + 127) // 128 * 4), dtype=torch.uint8,
+                                 device=device)
+        ck._q = ck._scale = None
+        ck._shape, ck._store = (tokens, cols), store
+        at = ck._buffer.data_ptr()
+        ck._c = _lib.Ckpt(at, at + size, tokens, cols, _FORMAT_CODES[store])
         return ck
+
+    def _split(self):
+        tokens, cols = self._shape
+        size = tokens * _lib.ckpt_q_pitch(cols)
+        self._q = self._buffer[:size].view(self._store).view(tokens, _lib.ckpt_q_pitch(cols))
+        self._scale = self._buffer[size:].view(tokens, _lib.ckpt_scale_pitch(cols))
 
     @property
     def q(self) -> torch.Tensor:
+        if self._q is None:
+            self._split()
         return self._q
 
     @property
     def scale(self) -> torch.Tensor:
+        if self._scale is None:
+            self._split()
         return self._scale
 
     @property
-    def cols(self) -> int:
-        return self._cols
+    def tokens(self) -> int:
+        return self._shape[0]
 
     @property
-    def tokens(self) -> int:
-        return self._q.shape[0]
+    def cols(self) -> int:
+        return self._shape[1]
 
     @property
     def shape(self):
-        return (self._q.shape[0], self._cols)
+        return self._shape
 
     @property
     def format(self) -> str:
-        return _FORMAT_NAMES[self._q.dtype]
+        return _FORMAT_NAMES[self._store]
 
     @property
     def device(self) -> torch.device:
-        return self._q.device
+        return (self._q if self._buffer is None else self._buffer).device
 
     @property
     def nbytes(self) -> int:
@@ -183,22 +200,27 @@ def _as_checkpoint(name, spec, shape, device) -> Optional[ActCheckpoint]:
         return ActCheckpoint.empty(*shape, fmt=spec, device=device)
     if not isinstance(spec, ActCheckpoint):
         raise TypeError(f"{name} must be a format name or an ActCheckpoint")
-    if spec.shape != tuple(shape) or spec.device != device:
+    if spec._shape != tuple(shape) or spec.device != device:
         raise ValueError(f"{name} is {spec}, expected {shape[0]} x {shape[1]} on {device}")
     return spec
 
 
 def _ref(ck):
+    """The library's descriptor of a checkpoint, by reference."""
     if ck is None:
         return None
-    return ctypes.byref(_lib.Ckpt(ck._q.data_ptr(), ck._scale.data_ptr(), ck._q.shape[0], ck._cols,
-                                  ck._code))
+    if ck._c is not None:      # of its own buffer
+        return ctypes.byref(ck._c)
+    return ctypes.byref(_lib.Ckpt(ck._q.data_ptr(), ck._scale.data_ptr(), *ck._shape,
+                                  _FORMAT_CODES[ck._store]))
 
 
-@_on_device
-def checkpoint_save(x: torch.Tensor, fmt: str = "e4m3", *, out: Optional[ActCheckpoint] = None) -> ActCheckpoint:
+def checkpoint_save(x: torch.Tensor, fmt: str = "e4m3", *, out: Optional[ActCheckpoint] = None,
+                    stream=None) -> ActCheckpoint:
     """Keeps ``x`` [tokens, cols] in 8 bits, ``fmt`` "e4m3" or "int8" (or in
     the format of ``out``)."""
+    if _away(x, stream):
+        return _there(checkpoint_save, x, stream, fmt, out=out)
     ld = _check_rows("x", x)
     dt = dtype_code(x.dtype)
     ck = _as_checkpoint("out", fmt if out is None else out, tuple(x.shape), x.device)
@@ -207,21 +229,28 @@ def checkpoint_save(x: torch.Tensor, fmt: str = "e4m3", *, out: Optional[ActChec
     return ck
 
 
-@_on_device
 def checkpoint_restore(ck: ActCheckpoint, dtype: torch.dtype = torch.bfloat16, *,
-                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values a checkpoint stands for (exact in bfloat16 and float32)."""
     if not isinstance(ck, ActCheckpoint):
         raise TypeError("ck must be an ActCheckpoint")
+    if _away(ck, stream):
+        return _there(checkpoint_restore, ck, stream, dtype, out=out)
     dt = dtype_code(dtype if out is None else out.dtype)
     if out is None:
-        out = torch.empty(ck.shape, dtype=dtype, device=ck.device)
+        out = torch.empty(ck._shape, dtype=dtype, device=ck.device)
     else:
         _check_rows("out", out, ck.device, ck.shape, contiguous=True)
     st = _lib.lib().muon_checkpoint_restore(_ref(ck), out.data_ptr(), dt,
                                             _raw_stream(ck.device.index))
     _check(st, "muon_checkpoint_restore")
     return out
+
+
+def _empty_rows(t):
+    """A new contiguous matrix like ``t``."""
+    return torch.empty_like(t) if t.is_contiguous() else \
+        torch.empty(tuple(t.shape), dtype=t.dtype, device=t.device)
 
 
 class LayerNormOut(NamedTuple):
@@ -232,8 +261,8 @@ class LayerNormOut(NamedTuple):
     y_checkpoint: Optional[ActCheckpoint]
 
 
-@_on_device
-def layernorm_forward(x, gain, bias=None, *, eps=1e-5, x_checkpoint=None, y_checkpoint=None) -> LayerNormOut:
+def layernorm_forward(x, gain, bias=None, *, eps=1e-5, x_checkpoint=None, y_checkpoint=None,
+                      stream=None) -> LayerNormOut:
     """``y = (x - mean) * rstd * gain + bias`` over the columns of ``x``.
 
     gain, bias: [cols], of one dtype (that of x or the other).  mean and rstd
@@ -241,6 +270,9 @@ def layernorm_forward(x, gain, bias=None, *, eps=1e-5, x_checkpoint=None, y_chec
     x.  ``x_checkpoint`` / ``y_checkpoint``: a format name, or an
     ActCheckpoint to overwrite, saves x, or y as returned, in the same pass.
     """
+    if _away(x, stream):
+        return _there(layernorm_forward, x, stream, gain, bias, eps=eps, x_checkpoint=x_checkpoint,
+                      y_checkpoint=y_checkpoint)
     ld = _check_rows("x", x)
     dt, dev = dtype_code(x.dtype), x.device
     tokens, cols = x.shape
@@ -250,7 +282,7 @@ def layernorm_forward(x, gain, bias=None, *, eps=1e-5, x_checkpoint=None, y_chec
         _check_vector("bias", bias, cols, dev, gain.dtype)
     xc = _as_checkpoint("x_checkpoint", x_checkpoint, (tokens, cols), dev)
     yc = _as_checkpoint("y_checkpoint", y_checkpoint, (tokens, cols), dev)
-    y = torch.empty((tokens, cols), dtype=x.dtype, device=dev)
+    y = _empty_rows(x)
     mean = torch.empty(tokens, dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
     st = _lib.lib().muon_layernorm_forward(
@@ -264,15 +296,17 @@ def layernorm_workspace_bytes(tokens: int, cols: int) -> int:
     return int(_lib.lib().muon_layernorm_workspace_bytes(tokens, cols))
 
 
-@_on_device
 def layernorm_backward(dy, x, gain, mean, rstd, *, bias=True, dgain=None, dbias=None,
-                       accumulate=False, workspace=None):
+                       accumulate=False, workspace=None, stream=None):
     """``(dx, dgain, dbias)`` of :func:`layernorm_forward`.
 
     x: the forward's input, or an ActCheckpoint of it.  dgain and dbias have
     the dtype of gain; given ones are overwritten, or added to with
     ``accumulate``.  ``bias=False`` skips dbias (None is returned).
     """
+    if _away(dy, stream):
+        return _there(layernorm_backward, dy, stream, x, gain, mean, rstd, bias=bias, dgain=dgain,
+                      dbias=dbias, accumulate=accumulate, workspace=workspace)
     ldy = _check_rows("dy", dy)
     dt, dev = dtype_code(dy.dtype), dy.device
     tokens, cols = dy.shape
@@ -293,7 +327,7 @@ def layernorm_backward(dy, x, gain, mean, rstd, *, bias=True, dgain=None, dbias=
             _check_vector(name, t, cols, dev, gain.dtype)
         elif accumulate and wanted:
             raise ValueError(f"accumulate needs {name}")
-    dx = torch.empty(tokens, cols, dtype=dy.dtype, device=dev)
+    dx = _empty_rows(dy)
     if dgain is None:
         dgain = torch.empty_like(gain)
     if bias and dbias is None:
@@ -315,8 +349,8 @@ def weight_grad_workspace_bytes(count: int, with_offsets: bool, tokens: int, row
                                                            cols, dtype_code(dtype)))
 
 
-@_on_device
-def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, workspace=None):
+def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, workspace=None,
+                stream=None):
     """Gradient of the weight of ``y = x W^T`` from ``dy`` [tokens, rows] and
     the checkpoint of ``x`` [tokens, cols]: ``G = dy^T x`` [rows, cols].
 
@@ -327,6 +361,9 @@ def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, w
     the device.  G: written in place (added to with ``accumulate``), or a new
     tensor of ``dtype`` (default: that of dy).
     """
+    if _away(dy, stream):
+        return _there(weight_grad, dy, stream, ck, offsets=offsets, G=G, dtype=dtype,
+                      accumulate=accumulate, workspace=workspace)
     ld = _check_rows("dy", dy)
     dt, dev = dtype_code(dy.dtype), dy.device
     tokens, rows = dy.shape
