@@ -269,6 +269,22 @@ __device__ __forceinline__ void unpack_bf16(uint32_t w, float up, int fmt, uint3
   o[1] = f2bf2(v[2], v[3]);
 }
 
+// The leading 8 bits of each of 8 values as bf16, which are taken off them: three
+// calls give all 24 bits of float32 values.  An infinity leaves no remainder.
+__device__ __forceinline__ u32x4_t take_part(float (&v)[8]) {
+  u32x4_t w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = __float_as_uint(v[2 * i]) & 0xffff0000u;
+    const uint32_t b = __float_as_uint(v[2 * i + 1]) & 0xffff0000u;
+    w[i] = (a >> 16) | b;
+    const float fa = __uint_as_float(a), fb = __uint_as_float(b);
+    v[2 * i] = v[2 * i] == fa ? 0.f : v[2 * i] - fa;
+    v[2 * i + 1] = v[2 * i + 1] == fb ? 0.f : v[2 * i + 1] - fb;
+  }
+  return w;
+}
+
 // Byte address of the 8 columns `chunk` of token row k in a [BK][128] tile.
 __device__ __forceinline__ int tile_at(int k, int chunk) {
   return k * (BN * 2) + ((chunk ^ gswz(k)) << 4);
@@ -295,70 +311,64 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
   const int wm = wave >> 1, wn = wave & 1;
 
   // This thread's part of a step: 8 columns of dy of two tokens, 16 of x of one.
+  // D steps are in flight, each in registers of its own.
+  constexpr int D = BF16 ? 4 : 2;
   const int yk = t >> 4, yc = t & 15;
   const int xk = t >> 3, xc = t & 7;
   using T = typename RowVec<BF16>::T;
-  constexpr int N = RowVec<BF16>::N;
-  float y[2][8];
-  uint32_t xr[4];
-  int xs;
-  auto load = [&](int k0) {
+  constexpr int N = RowVec<BF16>::N, W = 8 / N;   // vectors per 8 columns
+  u32x4_t y[D][2][W], q[D];
+  int scale[D];
+  // EASY: no vector crosses the end of a row, so that every lane loads (its
+  // last vector, the last token, where its own lies past the end; those of dy
+  // are zeroed when they are written, and columns past the end reach nothing
+  // that is stored).  Loads that no branch guards can be waited for one step at
+  // a time.
+  auto load = [&](auto easy, auto slot, int k0) __attribute__((always_inline)) {
+    constexpr int I = decltype(slot)::value;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = k0 + yk + 16 * h;
-      const T* row = static_cast<const T*>(p.dy) + int64_t(k) * p.lddy;
+      const T* row = static_cast<const T*>(p.dy) + int64_t(k < pc.end ? k : pc.end - 1) * p.lddy;
 #pragma unroll
-      for (int i = 0; i < 8; i += N) {
-        if (k < pc.end) {
-          load_vec<BF16>(row, i0 + yc * 8 + i, p.rows, y[h] + i);
-        } else {
-#pragma unroll
-          for (int c = 0; c < N; ++c) y[h][i + c] = 0.f;
-        }
+      for (int i = 0; i < W; ++i) {
+        const int col = i0 + yc * 8 + i * N;
+        if constexpr (decltype(easy)::value)
+          y[I][h][i] = load_raw<BF16, true>(row + (col < p.rows ? col : p.rows - N), 0, N);
+        else
+          y[I][h][i] = load_raw<BF16>(row, col, p.rows);
       }
     }
     const int k = k0 + xk, col = j0 + xc * 16;
-    xr[0] = xr[1] = xr[2] = xr[3] = 0;
-    xs = 0;
-    if (k < pc.end && col < p.x.q_pitch) {
-      const uint4 w = *reinterpret_cast<const uint4*>(p.x.q + int64_t(k) * p.x.q_pitch + col);
-      xr[0] = w.x;
-      xr[1] = w.y;
-      xr[2] = w.z;
-      xr[3] = w.w;
-      xs = p.x.scale[int64_t(k) * p.x.s_pitch + col / MUON_CKPT_BLOCK];
-    }
+    const int64_t token = k < pc.end ? k : pc.end - 1;
+    const int at = col < p.x.q_pitch ? col : int(p.x.q_pitch) - 16;
+    q[I] = *reinterpret_cast<const u32x4_t*>(p.x.q + token * p.x.q_pitch + at);
+    scale[I] = p.x.scale[token * p.x.s_pitch + at / MUON_CKPT_BLOCK];
   };
-  auto write = [&](int buf) {
+  auto write = [&](auto slot, int buf, int k0) __attribute__((always_inline)) {
+    constexpr int I = decltype(slot)::value;
     LDS_AS char* s = smem + buf * STAGE;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float v[8];
+      if (k0 + yk + 16 * h >= pc.end) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = y[h][i];
+        for (int i = 0; i < W; ++i) y[I][h][i] = u32x4_t{0, 0, 0, 0};
+      }
+      if constexpr (BF16) {
+        *reinterpret_cast<LDS_AS u32x4_t*>(s + tile_at(yk + 16 * h, yc)) = y[I][h][0];
+      } else {
+        float v[8];
 #pragma unroll
-      for (int part = 0; part < P; ++part) {
-        uint32_t w[4];
+        for (int i = 0; i < W; ++i) unpack_raw<false>(y[I][h][i], v + i * N);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // the leading 8 bits of each value; an infinity leaves no remainder
-          const uint32_t a = __float_as_uint(v[2 * i]) & 0xffff0000u;
-          const uint32_t b = __float_as_uint(v[2 * i + 1]) & 0xffff0000u;
-          w[i] = (a >> 16) | b;
-          if (part + 1 < P) {
-            const float fa = __uint_as_float(a), fb = __uint_as_float(b);
-            v[2 * i] = v[2 * i] == fa ? 0.f : v[2 * i] - fa;
-            v[2 * i + 1] = v[2 * i + 1] == fb ? 0.f : v[2 * i + 1] - fb;
-          }
-        }
-        *reinterpret_cast<LDS_AS u32x4_t*>(s + part * PLANE + tile_at(yk + 16 * h, yc)) =
-            u32x4_t{w[0], w[1], w[2], w[3]};
+        for (int part = 0; part < P; ++part)
+          *reinterpret_cast<LDS_AS u32x4_t*>(s + part * PLANE + tile_at(yk + 16 * h, yc)) = take_part(v);
       }
     }
-    const float up = ckpt_up(xs);
+    const float up = ckpt_up(scale[I]);
     uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpack_bf16(xr[i], up, p.x.fmt, o + 2 * i);
+    for (int i = 0; i < 4; ++i) unpack_bf16(q[I][i], up, p.x.fmt, o + 2 * i);
     LDS_AS char* sx = s + P * PLANE;
     *reinterpret_cast<LDS_AS u32x4_t*>(sx + tile_at(xk, 2 * xc)) = u32x4_t{o[0], o[1], o[2], o[3]};
     *reinterpret_cast<LDS_AS u32x4_t*>(sx + tile_at(xk, 2 * xc + 1)) = u32x4_t{o[4], o[5], o[6], o[7]};
@@ -373,14 +383,12 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
       for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
 
   const int steps = (pc.end - pc.begin + BK - 1) / BK;
-  if (steps > 0) {
-    load(pc.begin);
-    write(0);
-  }
-  __syncthreads();
-  for (int k = 0; k < steps; ++k) {
-    if (k + 1 < steps) load(pc.begin + (k + 1) * BK);
-    const LDS_AS char* s = smem + (k & 1) * STAGE;
+  // Step k, in slot I = k % D: its loads are in LDS; its slot takes those of step
+  // k + D, and the next slot's go to the other buffer.
+  auto step = [&](auto easy, auto slot, int k) __attribute__((always_inline)) {
+    constexpr int I = decltype(slot)::value;
+    if (k + D < steps) load(easy, slot, pc.begin + (k + D) * BK);
+    const LDS_AS char* s = smem + (I & 1) * STAGE;
 #pragma unroll
     for (int ks = 0; ks < BK / 16; ++ks) {
       bf16x8_t xf[2];
@@ -397,8 +405,45 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
             acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf[b], yf, acc[a][b], 0, 0, 0);
         }
     }
-    if (k + 1 < steps) write((k + 1) & 1);
-    __syncthreads();
+    if (k + 1 < steps)
+      write(std::integral_constant<int, (I + 1) % D>{}, (I + 1) & 1, pc.begin + (k + 1) * BK);
+    block_barrier();
+  };
+  static_assert(D % 2 == 0, "the buffer of a step follows from its slot");
+  std::integral_constant<int, 0> c0;
+  std::integral_constant<int, 1> c1;
+  std::integral_constant<int, 2 % D> c2;
+  std::integral_constant<int, 3 % D> c3;
+  auto run = [&](auto easy) __attribute__((always_inline)) {
+    load(easy, c0, pc.begin);
+    if (steps > 1) load(easy, c1, pc.begin + BK);
+    if constexpr (D > 2) {
+      if (steps > 2) load(easy, c2, pc.begin + 2 * BK);
+      if (steps > 3) load(easy, c3, pc.begin + 3 * BK);
+    }
+    write(c0, 0, pc.begin);
+    block_barrier();
+    int k = 0;
+    for (; k + 2 * D <= steps; k += D) {   // all loads of steps that there are
+      step(easy, c0, k);
+      step(easy, c1, k + 1);
+      if constexpr (D > 2) step(easy, c2, k + 2);
+      if constexpr (D > 2) step(easy, c3, k + 3);
+    }
+    for (; k < steps; k += D) {
+      step(easy, c0, k);
+      if (k + 1 < steps) step(easy, c1, k + 1);
+      if constexpr (D > 2) {
+        if (k + 2 < steps) step(easy, c2, k + 2);
+        if (k + 3 < steps) step(easy, c3, k + 3);
+      }
+    }
+  };
+  if (steps > 0) {
+    if (p.rows % N == 0 || i0 + BM <= p.rows)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
   }
 
   if (pc.parts == 1 && steps == 0 && p.accumulate) return;
@@ -725,21 +770,8 @@ __global__ __launch_bounds__(kThreads) void repack_kernel(const void* dy, int64_
 #pragma unroll
     for (int j = 0; j < 8; j += N) load_vec<BF16>(static_cast<const T*>(dy) + t * lddy, col + j, rows, v + j);
 #pragma unroll
-    for (int part = P - 1; part >= 0; --part) {   // the smallest part first in memory
-      u32x4_t w;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t a = __float_as_uint(v[2 * j]) & 0xffff0000u;
-        const uint32_t b = __float_as_uint(v[2 * j + 1]) & 0xffff0000u;
-        w[j] = (a >> 16) | b;
-        if (part > 0) {
-          const float fa = __uint_as_float(a), fb = __uint_as_float(b);
-          v[2 * j] = v[2 * j] == fa ? 0.f : v[2 * j] - fa;
-          v[2 * j + 1] = v[2 * j + 1] == fb ? 0.f : v[2 * j + 1] - fb;
-        }
-      }
-      *reinterpret_cast<u32x4_t*>(out + part * out_part + t * out_ld + col) = w;
-    }
+    for (int part = P - 1; part >= 0; --part)   // the smallest part first in memory
+      *reinterpret_cast<u32x4_t*>(out + part * out_part + t * out_ld + col) = take_part(v);
   }
 }
 
@@ -795,24 +827,27 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const WeightGrad p, int6
 
 int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
-
 // Parts that a matrix of `tokens` is cut into, `count` matrices at once: the
 // estimate below at its least.  In microseconds, measured on one MI355X: a
-// round of blocks (one per CU) takes 6 (start, first loads, stores) and 0.6
-// for each step on a quarter of the CUs, 0.95 on all of them; the join takes
-// 4 and, through the Infinity Cache, moves 8 bytes per element and part at
-// 10 TB/s.  4096 x 1024 over 16384 tokens, 64 tiles: 182 us in 2 parts, 131 in 4,
-// 151 in 8.  `steps_of`: steps of 32 tokens (three for float32 dy).
-int64_t parts_of(int64_t count, int64_t tokens, int64_t rows, int64_t cols, int64_t tiles,
-                 int steps_of) {
-  const double steps = double(cdiv(tokens, BK) * steps_of);
-  const double g = double(count) * double(rows) * double(cols);
+// round of blocks (one of the 256 x 256 tiles per CU, two of the 128 x 128)
+// takes 6 (start, first loads, stores); a step of 32 tokens 0.6 on a quarter of
+// the CUs and 0.95 on all of them (128 x 128: 0.75, float32 1.2); the partial
+// sums are written at 5 TB/s and joined, through the Infinity Cache, at 10,
+// after 4 (3) for the launch and, for the small matrices, 0.2 per part, each
+// a read that waits for memory.  4096 x 1024 over 16384 tokens: 182 us in 2
+// parts, 131 in 4, 151 in 8; 512 x 512: 83 in 4, 39 in 16, 36 in 32, 46 in 64;
+// 300 x 300 over 300: 18.6 in 1, 12.9 in 3.
+int64_t parts_of(int64_t count, int64_t tokens, int64_t rows, int64_t cols, bool wide, bool bf16) {
+  const int64_t tiles = wide ? cdiv(rows, Wide::BM) * cdiv(cols, Wide::BN) : cdiv(rows, BM) * cdiv(cols, BN);
+  const int64_t at_once = wide ? 256 : 512;
+  const double steps = double(cdiv(tokens, BK) * (wide && !bf16 ? 3 : 1));
+  const double g = double(count) * double(rows) * double(cols), join = wide ? 4 : 3;
   int64_t best = 1;
   double least = 0;
   for (int64_t n = 1; n <= 64 && n <= cdiv(tokens, 4 * BK); ++n) {
-    const double blocks = double(count * tiles * n), rounds = double(cdiv(count * tiles * n, 256));
-    const double step = 0.48 + 0.47 * std::min(1.0, blocks / 256);
-    const double us = rounds * (6 + step * steps / double(n)) + (n > 1 ? 4 + g * double(n) * 8 / 1e7 : 0);
+    const double blocks = double(count * tiles * n), rounds = double(cdiv(count * tiles * n, at_once));
+    const double step = wide ? 0.48 + 0.47 * std::min(1.0, blocks / 256) : bf16 ? 0.75 : 1.2;
+    const double us = rounds * (6 + step * steps / double(n)) + (n > 1 ? join + double(n) * (wide ? 0 : 0.2) + g * double(n) * 12 / 1e7 : 0);
     if (n == 1 || us < least) {
       best = n;
       least = us;
@@ -841,7 +876,7 @@ WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int
   if (w.wide && !(bf16 && rows % 8 == 0))
     w.repack_bytes = size_t(tokens) * size_t(cdiv(rows, 8) * 8) * (bf16 ? 2 : 6);
   const int64_t even = cdiv(tokens, count);
-  int64_t chunk = cdiv(even, parts_of(count, even, rows, cols, tiles, bf16 ? 1 : 3));
+  int64_t chunk = cdiv(even, parts_of(count, even, rows, cols, w.wide, bf16));
   if (ragged) chunk = std::max(chunk, tokens / 256 * tiles);
   chunk = std::max<int64_t>(4 * BK, cdiv(std::min(chunk, MUON_MAX_TOKENS), BK) * BK);
   w.chunk = uint32_t(chunk);
