@@ -79,7 +79,8 @@ ROOT = os.path.dirname(os.path.abspath(__file__))
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "ns_update_{}_hbm_traffic.md")
 # The sources the update kernel is built from: traffic counters are only
 # reported while these are unchanged since the counters were taken.
-KERNEL_SOURCES = ("muon_step_03_amd/csrc/k_ns_bf16.hip", "muon_step_03_amd/csrc/muon_internal.h")
+KERNEL_SOURCES = ("muon_step_03_amd/csrc/k_ns_bf16.hip", "muon_step_03_amd/csrc/lds_tiles.h",
+                  "muon_step_03_amd/csrc/muon_internal.h")
 COPY_BYTES = 256 * 1024 * 1024
 
 

@@ -762,7 +762,6 @@ namespace muon {
 
 void note_hip_error(hipError_t e) { g_last_hip_error = int(e); }
 bool debug_sync_enabled() { return debug_sync(); }
-int compute_units() { return 8 * cus_per_xcd(); }
 void trace_push(const char* name) {
   if (const Roctx* t = roctx()) t->push(name);
 }

@@ -308,7 +308,6 @@ hipError_t launch_adamw(const AdamBatch& bt, bool bf16, hipStream_t s);
 // Shared by the entry points of the other host files.
 void note_hip_error(hipError_t e);      // kept for muon_last_hip_error
 bool debug_sync_enabled();              // MUON_DEBUG
-int compute_units();                    // of the current device (0 on a HIP error)
 void trace_push(const char* name);      // roctx range, when MUON_TRACE is set
 void trace_pop();
 
