@@ -75,7 +75,8 @@
  *           only: it breaks the no-synchronisation rule above).
  *           MUON_TRACE=1 opens a roctx range around every Muon and AdamW
  *           call ("muon_step", "muon_adamw_step") and one per launch, named
- *           by its phase (see muon_profile_read), for rocprofv3
+ *           by its phase (see muon_profile_read), and one around every call
+ *           of a layer operator, named by the function, for rocprofv3
  *           --marker-trace; the roctx library is loaded at first use, and
  *           a message on stderr says so if it cannot be.
  */

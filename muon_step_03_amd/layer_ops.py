@@ -42,6 +42,8 @@ def _away(t, stream) -> bool:
 
 def _there(fn, t, stream, *args, **kw):
     """``fn(t, ...)`` with the device of ``t``, and ``stream`` if given, current."""
+    if not isinstance(t, (torch.Tensor, ActCheckpoint)):
+        raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
     if stream is None:
         with torch.cuda.device(t.device):
             return fn(t, *args, **kw)
@@ -102,6 +104,14 @@ def _workspace(need, device, workspace):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def _wrote(*given):
+    """Tells autograd that tensors it did not make were written: a backward
+    pass that kept one of them then raises, as after PyTorch's own writes."""
+    for t in given:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 class ActCheckpoint:
     """A tokens x cols activation kept in 8 bits (``include/muon.h``,
     "Checkpoint format"): ``q`` [tokens, cols up to a multiple of 32] in
@@ -151,6 +161,12 @@ class ActCheckpoint:
         size = tokens * _lib.ckpt_q_pitch(cols)
         self._q = self._buffer[:size].view(self._store).view(tokens, _lib.ckpt_q_pitch(cols))
         self._scale = self._buffer[size:].view(tokens, _lib.ckpt_scale_pitch(cols))
+
+    def __reduce__(self):      # copies and pickles have tensors of their own
+        return ActCheckpoint, (self.q, self.scale, self.cols)
+
+    def _written(self):
+        _wrote(*((self._q, self._scale) if self._buffer is None else (self._buffer,)))
 
     @property
     def q(self) -> torch.Tensor:
@@ -226,6 +242,8 @@ def checkpoint_save(x: torch.Tensor, fmt: str = "e4m3", *, out: Optional[ActChec
     ck = _as_checkpoint("out", fmt if out is None else out, tuple(x.shape), x.device)
     st = _lib.lib().muon_checkpoint_save(x.data_ptr(), ld, dt, _ref(ck), _raw_stream(x.device.index))
     _check(st, "muon_checkpoint_save")
+    if out is not None:
+        ck._written()
     return ck
 
 
@@ -236,14 +254,15 @@ def checkpoint_restore(ck: ActCheckpoint, dtype: torch.dtype = torch.bfloat16, *
         raise TypeError("ck must be an ActCheckpoint")
     if _away(ck, stream):
         return _there(checkpoint_restore, ck, stream, dtype, out=out)
-    dt = dtype_code(dtype if out is None else out.dtype)
+    given = out
     if out is None:
         out = torch.empty(ck._shape, dtype=dtype, device=ck.device)
     else:
         _check_rows("out", out, ck.device, ck.shape, contiguous=True)
-    st = _lib.lib().muon_checkpoint_restore(_ref(ck), out.data_ptr(), dt,
+    st = _lib.lib().muon_checkpoint_restore(_ref(ck), out.data_ptr(), dtype_code(out.dtype),
                                             _raw_stream(ck.device.index))
     _check(st, "muon_checkpoint_restore")
+    _wrote(given)
     return out
 
 
@@ -289,6 +308,10 @@ def layernorm_forward(x, gain, bias=None, *, eps=1e-5, x_checkpoint=None, y_chec
         x.data_ptr(), ld, gain.data_ptr(), _ptr(bias), tokens, cols, dt, pdt, float(eps),
         y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ref(xc), _ref(yc), _raw_stream(dev.index))
     _check(st, "muon_layernorm_forward")
+    if xc is x_checkpoint and xc is not None:
+        xc._written()
+    if yc is y_checkpoint and yc is not None:
+        yc._written()
     return LayerNormOut(y, mean, rstd, xc, yc)
 
 
@@ -328,6 +351,7 @@ def layernorm_backward(dy, x, gain, mean, rstd, *, bias=True, dgain=None, dbias=
         elif accumulate and wanted:
             raise ValueError(f"accumulate needs {name}")
     dx = _empty_rows(dy)
+    given = dgain, dbias
     if dgain is None:
         dgain = torch.empty_like(gain)
     if bias and dbias is None:
@@ -339,6 +363,7 @@ def layernorm_backward(dy, x, gain, mean, rstd, *, bias=True, dgain=None, dbias=
         dx.data_ptr(), dgain.data_ptr(), _ptr(dbias), int(accumulate), at, size,
         _raw_stream(dev.index))
     _check(st, "muon_layernorm_backward")
+    _wrote(*given)
     return dx, dgain, dbias
 
 
@@ -390,6 +415,7 @@ def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, w
             raise ValueError(f"G must be a contiguous tensor of shape {shape} on {dev}")
         if dtype is not None and G.dtype != dtype:
             raise TypeError(f"G has dtype {G.dtype}, expected {dtype}")
+    given = G
     gdt = dtype_code(G.dtype if G is not None else dtype or dy.dtype)
     if G is None:
         G = torch.empty(shape, dtype=dtype or dy.dtype, device=dev)
@@ -401,4 +427,5 @@ def weight_grad(dy, ck, *, offsets=None, G=None, dtype=None, accumulate=False, w
         dy.data_ptr(), ld, dt, _ref(ck), _ptr(offsets), count, rows, G.data_ptr(), gdt,
         int(accumulate), at, size, _raw_stream(dev.index))
     _check(st, "muon_weight_grad")
+    _wrote(given)
     return G

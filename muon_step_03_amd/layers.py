@@ -37,6 +37,7 @@ class _LayerNorm(torch.autograd.Function):
         out = layernorm_forward(rows, gain, bias, eps=eps, x_checkpoint=keep, y_checkpoint=y_keep)
         kept = (rows,) if keep is None else (out.x_checkpoint.q, out.x_checkpoint.scale)
         ctx.save_for_backward(gain, out.mean, out.rstd, *kept)
+        ctx.set_materialize_grads(False)      # no zeros for the checkpoint's outputs
         ctx.has_bias = bias is not None
         ctx.shape = x.shape
         y_kept = (None, None) if y_keep is None else (out.y_checkpoint.q, out.y_checkpoint.scale)
@@ -47,6 +48,8 @@ class _LayerNorm(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, _q, _scale):
+        if dy is None:
+            return (None,) * 6
         gain, mean, rstd, *kept = ctx.saved_tensors
         x = kept[0] if len(kept) == 1 else ActCheckpoint(*kept, ctx.shape[-1])
         dx, dgain, dbias = layernorm_backward(_rows(dy), x, gain, mean, rstd, bias=ctx.has_bias)
@@ -102,8 +105,8 @@ def linear(x, W, keep: Union[str, ActCheckpoint] = "e4m3"):
         with torch.autocast(device_type=x.device.type, enabled=False):
             return x @ W.t()      # no weight gradient: nothing is kept
     if isinstance(keep, ActCheckpoint):
-        if keep.shape != (x.numel() // max(1, x.shape[-1]), x.shape[-1]):
-            raise ValueError(f"keep is {keep}, x has shape {tuple(x.shape)}")
+        if keep.shape != (x.numel() // max(1, x.shape[-1]), x.shape[-1]) or keep.device != x.device:
+            raise ValueError(f"keep is {keep}, x has shape {tuple(x.shape)} on {x.device}")
     else:
         keep = checkpoint_save(_rows(x.detach()), keep)
     return _Linear.apply(x, W, keep.q, keep.scale)

@@ -1,4 +1,7 @@
 """The layer operators on the GPU against their float64 definitions."""
+import copy
+import pickle
+
 import numpy as np
 import pytest
 import torch
@@ -440,6 +443,90 @@ def test_captured_run():
         assert all(torch.equal(a, b) for a, b in zip(want, held)) and torch.equal(want_g, G)
 
 
+def test_two_streams_at_once():
+    """Calls on two streams, each with a workspace of its own."""
+    cases = [weight_case(6000, 520, 264, BF16, "int8", seed=s) for s in (1, 2)]
+    off = offsets_of([1000, 0, 5000]).to(DEV)
+    want = [M.weight_grad(dy, ck, offsets=off) for dy, ck, _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            got[i].append(M.weight_grad(*cases[i][:2], offsets=off, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(want[i], g) for i in (0, 1) for g in got[i])
+
+
+def test_more_matrices_than_the_plan_sorts():
+    counts = [1, 0, 3] * 500
+    dy, ck, x64 = weight_case(sum(counts), 24, 40, BF16, "e4m3")
+    off = offsets_of(counts)
+    check_weight(M.weight_grad(dy, ck, offsets=off.to(DEV)), dy, x64, off.tolist())
+
+
+def test_copies_of_a_checkpoint():
+    x = hidden(70, 200, BF16)
+    ck = M.checkpoint_save(x, "int8")
+    want = M.checkpoint_restore(ck)
+    copies = [copy.copy(ck), copy.deepcopy(ck), pickle.loads(pickle.dumps(ck)),
+              M.ActCheckpoint(ck.q.clone(), ck.scale.clone(), 200)]
+    copies.append(copy.deepcopy(copies[-1]))
+    M.checkpoint_save(torch.zeros_like(x), out=ck)
+    assert not M.checkpoint_restore(copies[0]).any()      # a shallow one shares its bytes
+    for c in copies[1:]:
+        assert c.format == "int8" and c.shape == (70, 200)
+        assert torch.equal(M.checkpoint_restore(c), want)
+
+
+# Rows whose bytes lie past 2^32 elements: the last ones have to be those of a
+# short call on the same rows.
+FAR, FAR_COLS = 131200, 32768
+
+
+def test_rows_past_32_bits():
+    x = torch.zeros(FAR, FAR_COLS, dtype=BF16, device=DEV)
+    x[-40:] = hidden(40, FAR_COLS, BF16)
+    gain, bias = params(FAR_COLS, BF16)
+    out = M.layernorm_forward(x, gain, bias, x_checkpoint="e4m3", y_checkpoint="int8")
+    near = M.layernorm_forward(x[-40:], gain, bias, x_checkpoint="e4m3", y_checkpoint="int8")
+    for a, b in zip(out[:3], near[:3]):
+        assert torch.equal(a[-40:], b)
+    for a, b in zip(out[3:], near[3:]):
+        assert torch.equal(a.q[-40:].view(torch.uint8), b.q.view(torch.uint8))
+        assert torch.equal(a.scale[-40:], b.scale)
+    assert torch.equal(M.checkpoint_restore(out.x_checkpoint)[-40:],
+                       M.checkpoint_restore(near.x_checkpoint))
+    saved = M.checkpoint_save(x)
+    assert torch.equal(saved.q.view(torch.uint8), out.x_checkpoint.q.view(torch.uint8))
+    # the other rows' dy is zero, and so is what they add
+    dy = torch.zeros_like(x)
+    dy[-40:] = grads(40, FAR_COLS, BF16)
+    far = M.layernorm_backward(dy, saved, gain, out.mean, out.rstd)
+    close = M.layernorm_backward(dy[-40:], near.x_checkpoint, gain, near.mean, near.rstd)
+    assert torch.equal(far[0][-40:], close[0]) and not far[0][:-40].any()
+    check_backward((close[0], far[1], far[2]), dy[-40:], lo.checkpoint(f64(x[-40:]), "e4m3")[0],
+                   gain, near.mean, near.rstd)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cols,rows", [(8, FAR_COLS), (8, FAR_COLS - 1), (FAR_COLS, 8)])
+def test_weight_grad_past_32_bits(dtype, cols, rows):
+    """Whole numbers, so that no order of the sums matters: exact."""
+    g = torch.Generator().manual_seed(3)
+    x = torch.zeros(FAR, cols, dtype=BF16, device=DEV)
+    dy = torch.zeros(FAR, rows, dtype=dtype, device=DEV)
+    x[-40:] = torch.randint(-1, 2, (40, cols), generator=g).to(BF16).to(DEV)
+    dy[-40:] = torch.randint(-9, 10, (40, rows), generator=g).to(dtype).to(DEV)
+    ck = M.checkpoint_save(x, "int8")
+    want = dy[-40:].cpu().double().t() @ x[-40:].cpu().double()
+    assert torch.equal(M.weight_grad(dy, ck, dtype=F32).cpu().double(), want)
+    off = torch.tensor([0, FAR - 50, FAR - 50, FAR], dtype=torch.int64, device=DEV)
+    G = M.weight_grad(dy, ck, offsets=off, dtype=F32)
+    assert not G[:2].any() and torch.equal(G[2].cpu().double(), want)
+
+
 @pytest.mark.parametrize("call,error,match", [
     (lambda x, v, ck: M.layernorm_forward(x.t(), v), ValueError, "unit column stride"),
     (lambda x, v, ck: M.layernorm_forward(x, v[:-1]), ValueError, "gain has shape"),
@@ -460,6 +547,9 @@ def test_captured_run():
     (lambda x, v, ck: M.checkpoint_restore(ck, out=x.t()), ValueError, "shape"),
     (lambda x, v, ck: M.weight_grad(x[:7], ck), ValueError, "expected 7 x 64"),
     (lambda x, v, ck: M.weight_grad(x, x), TypeError, "ActCheckpoint"),
+    (lambda x, v, ck: M.checkpoint_save([1.0], stream=torch.cuda.Stream()), TypeError, "torch.Tensor"),
+    (lambda x, v, ck: M.checkpoint_save(x.cpu(), stream=torch.cuda.Stream()), ValueError, "stream is on"),
+    (lambda x, v, ck: M.checkpoint_restore(ck, out=[1.0]), TypeError, "torch.Tensor"),
     (lambda x, v, ck: M.weight_grad(x, ck, accumulate=True), ValueError, "needs G"),
     (lambda x, v, ck: M.weight_grad(x, ck, G=x), ValueError, "G must be"),
     (lambda x, v, ck: M.weight_grad(x, ck, offsets=torch.zeros(3, dtype=torch.int32, device=DEV)), TypeError, "int64"),

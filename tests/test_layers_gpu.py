@@ -121,6 +121,30 @@ def test_refusals():
         dx.float().sum().backward()
 
 
+def test_overwritten_checkpoint_is_noticed():
+    x, W, gain = hidden(8, 64, BF16), leaf(hidden(16, 64, BF16, seed=1)), leaf(hidden(1, 64, BF16)[0])
+    ck = M.checkpoint_save(x)
+    for write in (lambda c: M.checkpoint_save(2 * x, out=c),
+                  lambda c: M.layernorm_forward(x, gain.detach(), x_checkpoint=c)):
+        z = M.linear(x, W, ck)
+        write(ck)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            z.sum().backward()
+    y, yc = M.layer_norm(x, gain, y_keep="int8")
+    z = M.linear(y, W, yc)
+    M.checkpoint_save(x, out=yc)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.sum().backward()
+    kept = torch.empty(8, 64, dtype=BF16, device=DEV)
+    y = M.layer_norm(kept.copy_(x), gain)
+    M.checkpoint_restore(ck, out=kept)      # the norm's input, kept as it is
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with torch.inference_mode():
+        c = M.checkpoint_save(x)
+        assert M.checkpoint_save(x, out=c) is c
+
+
 def test_training_step_and_accumulated_micro_batches():
     """A small block trained by the hybrid optimizer, its hidden gradients
     formed once by autograd and once by accumulate_grad over micro-batches."""
