@@ -93,6 +93,10 @@ constexpr int fwd_threads() { return LPR < 256 ? 256 : LPR; }
 template <int LPR>
 constexpr int bwd_threads() { return LPR < 1024 ? 512 : 1024; }
 
+// Whether two blocks of the backward pass share a CU: their threads do, and the
+// registers (128 each) hold all but float32 rows of 16 values a lane.
+constexpr bool bwd_two_blocks(bool bf16, int lpr, int v) { return lpr < 1024 && (bf16 || v < 16); }
+
 // A sum of a parameter's gradient, to where it belongs.
 __device__ __forceinline__ void store_param(const LnBackward& p, int k, int col, float t) {
   void* out = k ? p.dbias : p.dgain;
@@ -106,9 +110,8 @@ __device__ __forceinline__ void store_param(const LnBackward& p, int k, int col,
   }
 }
 
-// EVEN: cols is a multiple of a vector's N elements, so that a vector lies
-// within the row or past it.
-template <bool BF16, bool EVEN, int LPR, int V>
+// END: how rows end (with a whole vector where cols is a multiple of N).
+template <bool BF16, RowEnd END, int LPR, int V>
 __global__ __launch_bounds__(fwd_threads<LPR>()) void ln_forward_kernel(const LnForward p) {
   using R = RowVec<BF16>;
   using T = typename R::T;
@@ -132,7 +135,7 @@ __global__ __launch_bounds__(fwd_threads<LPR>()) void ln_forward_kernel(const Ln
   auto load = [&](int64_t row, u32x4_t (&w)[NV]) {
     const T* x = static_cast<const T*>(p.x) + (row < p.tokens ? row : p.tokens - 1) * p.ldx;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) w[j] = load_raw<BF16, EVEN>(x, (j * LPR + lane) * N, p.cols);
+    for (int j = 0; j < NV; ++j) w[j] = load_ahead<BF16, END>(x, (j * LPR + lane) * N, p.cols);
   };
   u32x4_t next[HOLD ? NV : 1];
   const int64_t first = int64_t(blockIdx.x) * RPB + threadIdx.x / LPR;
@@ -153,6 +156,7 @@ __global__ __launch_bounds__(fwd_threads<LPR>()) void ln_forward_kernel(const Ln
     float s[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      settle<BF16, END>(w[j], (j * LPR + lane) * N, p.cols);
       unpack_raw<BF16>(w[j], v[j]);
 #pragma unroll
       for (int i = 0; i < N; ++i) s[0] += v[j][i];
@@ -170,7 +174,7 @@ __global__ __launch_bounds__(fwd_threads<LPR>()) void ln_forward_kernel(const Ln
 #pragma unroll
       for (int i = 0; i < N; ++i) v[j][i] -= mean;
       float t = 0.f;
-      if constexpr (!EVEN) {
+      if constexpr (END != END_WHOLE) {
         if (left < N) {
 #pragma unroll
           for (int i = 0; i < N; ++i)
@@ -198,7 +202,7 @@ __global__ __launch_bounds__(fwd_threads<LPR>()) void ln_forward_kernel(const Ln
 #pragma unroll
       for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(v[j][i] * rstd, gain[k][i], bias[k][i]);
       u32x4_t out = pack_raw<BF16>(o);
-      store_raw<BF16, EVEN>(y, col, p.cols, out);
+      store_raw<BF16, END == END_WHOLE>(y, col, p.cols, out);
       // the checkpoint holds y as the next layer reads it
       if (p.yc.fmt >= 0) {
         if (col >= p.cols) out = u32x4_t{0, 0, 0, 0};
@@ -209,8 +213,9 @@ __global__ __launch_bounds__(fwd_threads<LPR>()) void ln_forward_kernel(const Ln
 }
 
 // CK: x from its checkpoint.
-template <bool BF16, bool EVEN, bool CK, int LPR, int V>
-__global__ __launch_bounds__(bwd_threads<LPR>()) void ln_backward_kernel(const LnBackward p) {
+template <bool BF16, RowEnd END, bool CK, int LPR, int V>
+__global__ __launch_bounds__(bwd_threads<LPR>(), bwd_two_blocks(BF16, LPR, V) ? 4 : 1)
+void ln_backward_kernel(const LnBackward p) {
   using R = RowVec<BF16>;
   using T = typename R::T;
   constexpr int N = R::N, NV = V / N, NT = bwd_threads<LPR>(), RPB = NT / LPR;
@@ -240,11 +245,11 @@ __global__ __launch_bounds__(bwd_threads<LPR>()) void ln_backward_kernel(const L
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int col = (j * LPR + lane) * N;
-      r.dy[j] = load_raw<BF16, EVEN>(static_cast<const T*>(p.dy) + at * p.lddy, col, p.cols);
+      r.dy[j] = load_ahead<BF16, END>(static_cast<const T*>(p.dy) + at * p.lddy, col, p.cols);
       if constexpr (CK)
         r.c[j] = ckpt_load<N>(p.xc, at, col);
       else
-        r.x[j] = load_raw<BF16, EVEN>(static_cast<const T*>(p.x) + at * p.ldx, col, p.cols);
+        r.x[j] = load_ahead<BF16, END>(static_cast<const T*>(p.x) + at * p.ldx, col, p.cols);
     }
   };
   const int64_t stride = int64_t(gridDim.x) * RPB;
@@ -265,11 +270,14 @@ __global__ __launch_bounds__(bwd_threads<LPR>()) void ln_backward_kernel(const L
     // past the row's end dy is zero, and so is every term of the sums
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      settle<BF16, END>(cur.dy[j], (j * LPR + lane) * N, p.cols);
       unpack_raw<BF16>(cur.dy[j], a[j]);
-      if constexpr (CK)
+      if constexpr (CK) {
         ckpt_values<N>(cur.c[j], p.xc.fmt, xh[j]);
-      else
+      } else {
+        settle<BF16, END>(cur.x[j], (j * LPR + lane) * N, p.cols);
         unpack_raw<BF16>(cur.x[j], xh[j]);
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i) xh[j][i] = (xh[j][i] - cur.mean) * cur.rstd;
       if (live) {
@@ -298,7 +306,7 @@ __global__ __launch_bounds__(bwd_threads<LPR>()) void ln_backward_kernel(const L
         float o[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = cur.rstd * (a[j][i] - c0 - xh[j][i] * c1);
-        store_raw<BF16, EVEN>(dx, (j * LPR + lane) * N, p.cols, pack_raw<BF16>(o));
+        store_raw<BF16, END == END_WHOLE>(dx, (j * LPR + lane) * N, p.cols, pack_raw<BF16>(o));
       }
     }
   }
@@ -345,8 +353,18 @@ __global__ __launch_bounds__(1024) void ln_params_kernel(const LnBackward p) {
   float t = 0.f;
   if (col < p.cols) {
     const float* in = p.partial + int64_t(k) * p.cols + col;
-#pragma unroll 16
-    for (int b = ty; b < p.blocks; b += 32) t += in[int64_t(b) * 2 * p.cols];
+    // 16 loads in flight whatever the number of rows (500 rows of 1411: 7.5 us
+    // when the last ones were loaded one by one)
+    for (int b0 = ty; b0 < p.blocks; b0 += 512) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int b = b0 + 32 * i;
+        v[i] = in[int64_t(b < p.blocks ? b : b0) * 2 * p.cols];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) t += b0 + 32 * i < p.blocks ? v[i] : 0.f;
+    }
   }
   part[ty][tx] = t;
   __syncthreads();
@@ -380,39 +398,47 @@ hipError_t forward(const LnForward& p, hipStream_t s) {
   const int64_t want = (p.tokens + RPB - 1) / RPB;
   const int64_t cap = 256 * (2048 / NT);   // the waves that fill the chip
   const dim3 grid(unsigned(want < cap ? want : cap)), block(NT);
-  if (p.cols % RowVec<BF16>::N == 0)
-    hipLaunchKernelGGL((ln_forward_kernel<BF16, true, LPR, V>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((ln_forward_kernel<BF16, false, LPR, V>), grid, block, 0, s, p);
+  const RowEnd end = row_end(p.cols, RowVec<BF16>::N);
+  if (end == END_WHOLE)
+    hipLaunchKernelGGL((ln_forward_kernel<BF16, END_WHOLE, LPR, V>), grid, block, 0, s, p);
+  else if (end == END_INSIDE)
+    hipLaunchKernelGGL((ln_forward_kernel<BF16, END_INSIDE, LPR, V>), grid, block, 0, s, p);
+  else if constexpr (LPR * V == 256)   // the shape of the shortest rows
+    hipLaunchKernelGGL((ln_forward_kernel<BF16, END_SHORT, LPR, V>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
-template <bool BF16, bool EVEN, int LPR, int V>
+template <bool BF16, RowEnd END, int LPR, int V>
 hipError_t backward_of(const LnBackward& p, hipStream_t s) {
   const dim3 grid(unsigned(p.blocks)), block(bwd_threads<LPR>());
   if (p.x)
-    hipLaunchKernelGGL((ln_backward_kernel<BF16, EVEN, false, LPR, V>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((ln_backward_kernel<BF16, END, false, LPR, V>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((ln_backward_kernel<BF16, EVEN, true, LPR, V>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((ln_backward_kernel<BF16, END, true, LPR, V>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 template <bool BF16, int LPR, int V>
 hipError_t backward(const LnBackward& p, hipStream_t s) {
-  return p.cols % RowVec<BF16>::N == 0 ? backward_of<BF16, true, LPR, V>(p, s)
-                                       : backward_of<BF16, false, LPR, V>(p, s);
+  const RowEnd end = row_end(p.cols, RowVec<BF16>::N);
+  if (end == END_WHOLE) return backward_of<BF16, END_WHOLE, LPR, V>(p, s);
+  if (end == END_INSIDE) return backward_of<BF16, END_INSIDE, LPR, V>(p, s);
+  if constexpr (LPR * V == 256) return backward_of<BF16, END_SHORT, LPR, V>(p, s);   // the shortest rows
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-// Two blocks of 512 threads per CU, or one of 1024.  Up to kOneBlock passes of
-// a block are left to a single one, which spares the second launch: 12 rows of
-// 768 in 5.4 us against 7.4, 64 in 8 passes in about the same as with it, but
-// at 3 us less of the host's time.
+// The blocks that the CUs hold at once (a third one would only wait: float32
+// rows of 1024, 4099 of them, 14.9 us with 512 blocks, one per CU at a time, 11.6
+// with 256).  Up to kOneBlock passes of a block are left to a single one, which
+// spares the second launch: 12 rows of 768 in 5.4 us against 7.4; 64 in 8 passes
+// take 11.3 us against 6.7, but 3 us less of the host's time, which is longer.
 constexpr int64_t kOneBlock = 8;
-int ln_backward_blocks(int64_t tokens, int64_t cols) {
-  const int lpr = row_shape(cols, true).lpr, nt = lpr < 1024 ? 512 : 1024;
-  const int64_t want = (tokens + nt / lpr - 1) / (nt / lpr);
-  const int64_t cap = 256 * (1024 / nt);
+int ln_backward_blocks(int64_t tokens, int64_t cols, bool bf16) {
+  const RowShape r = row_shape(cols, true);
+  const int nt = r.lpr < 1024 ? 512 : 1024, rows = nt / r.lpr;
+  const int64_t want = (tokens + rows - 1) / rows;
+  const int64_t cap = bwd_two_blocks(bf16, r.lpr, r.v) ? 512 : 256;
   return int(want < 1 ? 0 : want <= kOneBlock ? 1 : want < cap ? want : cap);
 }
 

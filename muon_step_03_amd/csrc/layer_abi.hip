@@ -197,7 +197,7 @@ int muon_layernorm_forward(const void* x, int64_t ldx, const void* gain, const v
 
 size_t muon_layernorm_workspace_bytes(int64_t tokens, int64_t cols) {
   if (!sizes_ok(tokens, cols)) return 0;
-  const int blocks = ln_backward_blocks(tokens, cols);
+  const int blocks = ln_backward_blocks(tokens, cols, true);   // enough for either type
   return blocks > 1 ? size_t(blocks) * 2 * size_t(cols) * 4 + kAlign : 0;
 }
 
@@ -252,7 +252,7 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
   p.cols = int(cols);
   p.param_bf16 = param_dtype == MUON_DTYPE_BF16;
   p.accumulate = accumulate != 0;
-  p.blocks = ln_backward_blocks(tokens, cols);
+  p.blocks = ln_backward_blocks(tokens, cols, dtype == MUON_DTYPE_BF16);
   Trace t("muon_layernorm_backward");
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (p.blocks > 0) {

@@ -108,6 +108,41 @@ __device__ __forceinline__ u32x4_t load_raw(const void* row, int col, int cols) 
   }
   return w;
 }
+
+// How rows end: with a whole vector; inside a vector of a row that holds one
+// at least; before the first vector's end.
+enum RowEnd { END_WHOLE, END_INSIDE, END_SHORT };
+inline RowEnd row_end(int64_t cols, int n) {
+  return cols % n == 0 ? END_WHOLE : cols >= n ? END_INSIDE : END_SHORT;
+}
+// load_raw in two halves, for loads in flight: what is loaded, and, once it is
+// used, the elements that were asked for.  A vector that crosses the row's end
+// (or lies past it) is loaded from the row's last N elements and shifted down:
+// a load that no lane's branch guards, which nothing has to wait for before its
+// use (16384 rows of 1411 float32, forward: 44 us with guarded elements, 35 so).
+template <bool BF16, RowEnd END>
+__device__ __forceinline__ u32x4_t load_ahead(const void* row, int col, int cols) {
+  if constexpr (END != END_INSIDE) return load_raw<BF16, END == END_WHOLE>(row, col, cols);
+  using R = RowVec<BF16>;
+  const int at = col < cols - R::N ? col : cols - R::N;
+  const typename R::Raw r =
+      *reinterpret_cast<const typename R::Raw*>(static_cast<const typename R::T*>(row) + at);
+  return u32x4_t{r[0], r[1], r[2], r[3]};
+}
+template <bool BF16, RowEnd END>
+__device__ __forceinline__ void settle(u32x4_t& w, int col, int cols) {
+  if constexpr (END != END_INSIDE) return;
+  int by = col - (cols - RowVec<BF16>::N);   // elements
+  if (by <= 0) return;
+  if constexpr (BF16) {
+    if (by & 1)
+      w = u32x4_t{w[0] >> 16 | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | w[3] << 16, w[3] >> 16};
+    by >>= 1;
+  }
+  if (by & 1) w = u32x4_t{w[1], w[2], w[3], 0};
+  if (by & 2) w = u32x4_t{w[2], w[3], 0, 0};
+  if (by >= 4) w = u32x4_t{0, 0, 0, 0};
+}
 template <bool BF16>
 __device__ __forceinline__ void unpack_raw(u32x4_t w, float* v) {
 #pragma unroll
@@ -340,7 +375,7 @@ struct LnBackward {
 };
 
 // Blocks of the backward's first launch: each leaves one row of partial sums.
-int ln_backward_blocks(int64_t tokens, int64_t cols);
+int ln_backward_blocks(int64_t tokens, int64_t cols, bool bf16);   // bf16: at least float32's
 
 hipError_t launch_ln_forward(const LnForward& p, bool bf16, hipStream_t s);
 hipError_t launch_ln_backward(const LnBackward& p, bool bf16, hipStream_t s);
