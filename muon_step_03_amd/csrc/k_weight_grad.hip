@@ -261,12 +261,24 @@ __device__ __forceinline__ void store_tile(const WeightGrad& p, const Piece& pc,
   }
 }
 
-// bf16 pairs of four checkpoint bytes (exact).
-__device__ __forceinline__ void unpack_bf16(uint32_t w, float up, int fmt, uint32_t* o) {
-  float v[4];
-  ckpt_unpack4(w, up, fmt, v);
-  o[0] = f2bf2(v[0], v[1]);
-  o[1] = f2bf2(v[2], v[3]);
+// Four checkpoint bytes -> four bf16, exact; a marked block gives NaN.
+template <int FMT>
+__device__ __forceinline__ void unpack4(uint32_t q, int byte, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == MUON_CKPT_E4M3) {
+    // the conversion scales by the exponent of `up`, 255 giving NaN
+    const float up = __uint_as_float(uint32_t(byte) << 23);
+    lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, up, false));
+    hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, up, true));
+  } else {
+    // bytes offset to unsigned, the offset taken off again in the scaling
+    const float up = ckpt_up(byte), off = -128.f * up;
+    const uint32_t w = q ^ 0x80808080u;
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(float((w >> (8 * j)) & 0xffu), up, off);
+    lo = f2bf2(v[0], v[1]);
+    hi = f2bf2(v[2], v[3]);
+  }
 }
 
 // The leading 8 bits of each of 8 values as bf16, which are taken off them: three
@@ -290,7 +302,7 @@ __device__ __forceinline__ int tile_at(int k, int chunk) {
   return k * (BN * 2) + ((chunk ^ gswz(k)) << 4);
 }
 
-template <bool BF16>
+template <bool BF16, int FMT>
 __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGrad p, int tiles_m,
                                                             int tiles_n) {
   constexpr int P = BF16 ? 1 : 3;            // bf16 parts of dy
@@ -365,10 +377,9 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
           *reinterpret_cast<LDS_AS u32x4_t*>(s + part * PLANE + tile_at(yk + 16 * h, yc)) = take_part(v);
       }
     }
-    const float up = ckpt_up(scale[I]);
     uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpack_bf16(q[I][i], up, p.x.fmt, o + 2 * i);
+    for (int i = 0; i < 4; ++i) unpack4<FMT>(q[I][i], scale[I], o[2 * i], o[2 * i + 1]);
     LDS_AS char* sx = s + P * PLANE;
     *reinterpret_cast<LDS_AS u32x4_t*>(sx + tile_at(xk, 2 * xc)) = u32x4_t{o[0], o[1], o[2], o[3]};
     *reinterpret_cast<LDS_AS u32x4_t*>(sx + tile_at(xk, 2 * xc + 1)) = u32x4_t{o[4], o[5], o[6], o[7]};
@@ -384,29 +395,38 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
 
   const int steps = (pc.end - pc.begin + BK - 1) / BK;
   // Step k, in slot I = k % D: its loads are in LDS; its slot takes those of step
-  // k + D, and the next slot's go to the other buffer.
-  auto step = [&](auto easy, auto slot, int k) __attribute__((always_inline)) {
+  // k + D, and the next slot's go to the other buffer.  END: there may be no such
+  // steps.  (Loads behind a branch would all be waited for at the next write.)
+  auto step = [&](auto easy, auto slot, auto end, int k) __attribute__((always_inline)) {
     constexpr int I = decltype(slot)::value;
-    if (k + D < steps) load(easy, slot, pc.begin + (k + D) * BK);
+    constexpr bool END = decltype(end)::value;
     const LDS_AS char* s = smem + (I & 1) * STAGE;
+    bf16x8_t xf[BK / 16][2], yf[BK / 16][P][2];
 #pragma unroll
     for (int ks = 0; ks < BK / 16; ++ks) {
-      bf16x8_t xf[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
-        xf[b] = lds_frag_xT<BN>(s + P * PLANE, ks * 16, wn * 64 + b * 32, lane);
+        xf[ks][b] = lds_frag_xT<BN>(s + P * PLANE, ks * 16, wn * 64 + b * 32, lane);
+#pragma unroll
+      for (int part = 0; part < P; ++part)
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+          yf[ks][part][a] = lds_frag_xT<BM>(s + part * PLANE, ks * 16, wm * 64 + a * 32, lane);
+    }
+    if (!END || k + D < steps) load(easy, slot, pc.begin + (k + D) * BK);
+#pragma unroll
+    for (int ks = 0; ks < BK / 16; ++ks) {
 #pragma unroll
       for (int part = P - 1; part >= 0; --part)
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const bf16x8_t yf = lds_frag_xT<BM>(s + part * PLANE, ks * 16, wm * 64 + a * 32, lane);
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
           for (int b = 0; b < 2; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf[b], yf, acc[a][b], 0, 0, 0);
-        }
+            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf[ks][b], yf[ks][part][a], acc[a][b],
+                                                                0, 0, 0);
+      if (ks == 0 && (!END || k + 1 < steps))
+        write(std::integral_constant<int, (I + 1) % D>{}, (I + 1) & 1, pc.begin + (k + 1) * BK);
     }
-    if (k + 1 < steps)
-      write(std::integral_constant<int, (I + 1) % D>{}, (I + 1) & 1, pc.begin + (k + 1) * BK);
     block_barrier();
   };
   static_assert(D % 2 == 0, "the buffer of a step follows from its slot");
@@ -424,18 +444,21 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
     write(c0, 0, pc.begin);
     block_barrier();
     int k = 0;
-    for (; k + 2 * D <= steps; k += D) {   // all loads of steps that there are
-      step(easy, c0, k);
-      step(easy, c1, k + 1);
-      if constexpr (D > 2) step(easy, c2, k + 2);
-      if constexpr (D > 2) step(easy, c3, k + 3);
-    }
-    for (; k < steps; k += D) {
-      step(easy, c0, k);
-      if (k + 1 < steps) step(easy, c1, k + 1);
+    for (; k + 2 * D <= steps; k += D) {
+      step(easy, c0, std::false_type{}, k);
+      step(easy, c1, std::false_type{}, k + 1);
       if constexpr (D > 2) {
-        if (k + 2 < steps) step(easy, c2, k + 2);
-        if (k + 3 < steps) step(easy, c3, k + 3);
+        step(easy, c2, std::false_type{}, k + 2);
+        step(easy, c3, std::false_type{}, k + 3);
+      }
+    }
+    std::true_type end;
+    for (; k < steps; k += D) {
+      step(easy, c0, end, k);
+      if (k + 1 < steps) step(easy, c1, end, k + 1);
+      if constexpr (D > 2) {
+        if (k + 2 < steps) step(easy, c2, end, k + 2);
+        if (k + 3 < steps) step(easy, c3, end, k + 3);
       }
     }
   };
@@ -488,26 +511,6 @@ __device__ __forceinline__ bf16x8_t frag_x(const LDS_AS char* tile, int kb, int 
   const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4_t*)(p0 + 4 * W * 2));
   const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   return __builtin_bit_cast(bf16x8_t, v);
-}
-
-// Four checkpoint bytes -> four bf16, exact; a marked block gives NaN.
-template <int FMT>
-__device__ __forceinline__ void unpack4(uint32_t q, int byte, uint32_t& lo, uint32_t& hi) {
-  if constexpr (FMT == MUON_CKPT_E4M3) {
-    // the conversion scales by the exponent of `up`, 255 giving NaN
-    const float up = __uint_as_float(uint32_t(byte) << 23);
-    lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, up, false));
-    hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, up, true));
-  } else {
-    // bytes offset to unsigned, the offset taken off again in the scaling
-    const float up = ckpt_up(byte), off = -128.f * up;
-    const uint32_t w = q ^ 0x80808080u;
-    float v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(float((w >> (8 * j)) & 0xffu), up, off);
-    lo = f2bf2(v[0], v[1]);
-    hi = f2bf2(v[2], v[3]);
-  }
 }
 
 // PARTS == 3: dy in three bf16 parts, a matrix of all tokens each (float32 dy);
@@ -898,6 +901,14 @@ WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int
   return w;
 }
 
+template <bool BF16>
+hipError_t launch_small(const WeightGrad& p, dim3 grid, int tm, int tn, hipStream_t s) {
+  if (p.x.fmt == MUON_CKPT_E4M3)
+    hipLaunchKernelGGL((weight_grad_kernel<BF16, MUON_CKPT_E4M3>), grid, dim3(kThreads), 0, s, p, tm, tn);
+  else
+    hipLaunchKernelGGL((weight_grad_kernel<BF16, MUON_CKPT_INT8>), grid, dim3(kThreads), 0, s, p, tm, tn);
+  return hipGetLastError();
+}
 template <int PARTS>
 hipError_t launch_wide(const WeightGrad& p, dim3 grid, int tm, int tn, hipStream_t s) {
   if (p.x.fmt == MUON_CKPT_E4M3)
@@ -949,11 +960,7 @@ hipError_t launch_weight_grad(const WeightGrad& call, const WeightGradPlan& plan
     return bf16 ? launch_wide<1>(p, grid(tm, tn), tm, tn, s) : launch_wide<3>(p, grid(tm, tn), tm, tn, s);
   }
   const int tm = int(cdiv(p.rows, BM)), tn = int(cdiv(p.cols, BN));
-  if (bf16)
-    hipLaunchKernelGGL(weight_grad_kernel<true>, grid(tm, tn), dim3(kThreads), 0, s, p, tm, tn);
-  else
-    hipLaunchKernelGGL(weight_grad_kernel<false>, grid(tm, tn), dim3(kThreads), 0, s, p, tm, tn);
-  return hipGetLastError();
+  return bf16 ? launch_small<true>(p, grid(tm, tn), tm, tn, s) : launch_small<false>(p, grid(tm, tn), tm, tn, s);
 }
 
 hipError_t launch_weight_grad_join(const WeightGrad& p, const WeightGradPlan& plan, hipStream_t s) {
