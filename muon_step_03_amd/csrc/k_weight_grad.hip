@@ -331,25 +331,20 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
   constexpr int N = RowVec<BF16>::N, W = 8 / N;   // vectors per 8 columns
   u32x4_t y[D][2][W], q[D];
   int scale[D];
-  // EASY: no vector crosses the end of a row, so that every lane loads (its
-  // last vector, the last token, where its own lies past the end; those of dy
-  // are zeroed when they are written, and columns past the end reach nothing
-  // that is stored).  Loads that no branch guards can be waited for one step at
-  // a time.
-  auto load = [&](auto easy, auto slot, int k0) __attribute__((always_inline)) {
+  // Every lane loads: tokens past the end the last one (their dy is zeroed when
+  // it is written), vectors past a row's end its last (columns past the end
+  // reach nothing that is stored; one that crosses it is shifted when written).
+  // Loads that no branch guards can be waited for one step at a time.
+  auto load = [&](auto end, auto slot, int k0) __attribute__((always_inline)) {
     constexpr int I = decltype(slot)::value;
+    constexpr RowEnd HOW = decltype(end)::value == END_SHORT ? END_SHORT : END_INSIDE;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = k0 + yk + 16 * h;
       const T* row = static_cast<const T*>(p.dy) + int64_t(k < pc.end ? k : pc.end - 1) * p.lddy;
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const int col = i0 + yc * 8 + i * N;
-        if constexpr (decltype(easy)::value)
-          y[I][h][i] = load_raw<BF16, true>(row + (col < p.rows ? col : p.rows - N), 0, N);
-        else
-          y[I][h][i] = load_raw<BF16>(row, col, p.rows);
-      }
+      for (int i = 0; i < W; ++i)
+        y[I][h][i] = load_ahead<BF16, HOW>(row, i0 + yc * 8 + i * N, p.rows);
     }
     const int k = k0 + xk, col = j0 + xc * 16;
     const int64_t token = k < pc.end ? k : pc.end - 1;
@@ -357,11 +352,13 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
     q[I] = *reinterpret_cast<const u32x4_t*>(p.x.q + token * p.x.q_pitch + at);
     scale[I] = p.x.scale[token * p.x.s_pitch + at / MUON_CKPT_BLOCK];
   };
-  auto write = [&](auto slot, int buf, int k0) __attribute__((always_inline)) {
+  auto write = [&](auto end, auto slot, int buf, int k0) __attribute__((always_inline)) {
     constexpr int I = decltype(slot)::value;
     LDS_AS char* s = smem + buf * STAGE;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) settle<BF16, decltype(end)::value>(y[I][h][i], i0 + yc * 8 + i * N, p.rows);
       if (k0 + yk + 16 * h >= pc.end) {
 #pragma unroll
         for (int i = 0; i < W; ++i) y[I][h][i] = u32x4_t{0, 0, 0, 0};
@@ -395,11 +392,11 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
 
   const int steps = (pc.end - pc.begin + BK - 1) / BK;
   // Step k, in slot I = k % D: its loads are in LDS; its slot takes those of step
-  // k + D, and the next slot's go to the other buffer.  END: there may be no such
+  // k + D, and the next slot's go to the other buffer.  LAST: there may be no such
   // steps.  (Loads behind a branch would all be waited for at the next write.)
-  auto step = [&](auto easy, auto slot, auto end, int k) __attribute__((always_inline)) {
+  auto step = [&](auto end, auto slot, auto last, int k) __attribute__((always_inline)) {
     constexpr int I = decltype(slot)::value;
-    constexpr bool END = decltype(end)::value;
+    constexpr bool LAST = decltype(last)::value;
     const LDS_AS char* s = smem + (I & 1) * STAGE;
     bf16x8_t xf[BK / 16][2], yf[BK / 16][P][2];
 #pragma unroll
@@ -413,7 +410,7 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
         for (int a = 0; a < 2; ++a)
           yf[ks][part][a] = lds_frag_xT<BM>(s + part * PLANE, ks * 16, wm * 64 + a * 32, lane);
     }
-    if (!END || k + D < steps) load(easy, slot, pc.begin + (k + D) * BK);
+    if (!LAST || k + D < steps) load(end, slot, pc.begin + (k + D) * BK);
 #pragma unroll
     for (int ks = 0; ks < BK / 16; ++ks) {
 #pragma unroll
@@ -424,8 +421,8 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
           for (int b = 0; b < 2; ++b)
             acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf[ks][b], yf[ks][part][a], acc[a][b],
                                                                 0, 0, 0);
-      if (ks == 0 && (!END || k + 1 < steps))
-        write(std::integral_constant<int, (I + 1) % D>{}, (I + 1) & 1, pc.begin + (k + 1) * BK);
+      if (ks == 0 && (!LAST || k + 1 < steps))
+        write(end, std::integral_constant<int, (I + 1) % D>{}, (I + 1) & 1, pc.begin + (k + 1) * BK);
     }
     block_barrier();
   };
@@ -434,39 +431,41 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
   std::integral_constant<int, 1> c1;
   std::integral_constant<int, 2 % D> c2;
   std::integral_constant<int, 3 % D> c3;
-  auto run = [&](auto easy) __attribute__((always_inline)) {
-    load(easy, c0, pc.begin);
-    if (steps > 1) load(easy, c1, pc.begin + BK);
+  auto run = [&](auto end) __attribute__((always_inline)) {
+    load(end, c0, pc.begin);
+    if (steps > 1) load(end, c1, pc.begin + BK);
     if constexpr (D > 2) {
-      if (steps > 2) load(easy, c2, pc.begin + 2 * BK);
-      if (steps > 3) load(easy, c3, pc.begin + 3 * BK);
+      if (steps > 2) load(end, c2, pc.begin + 2 * BK);
+      if (steps > 3) load(end, c3, pc.begin + 3 * BK);
     }
-    write(c0, 0, pc.begin);
+    write(end, c0, 0, pc.begin);
     block_barrier();
     int k = 0;
     for (; k + 2 * D <= steps; k += D) {
-      step(easy, c0, std::false_type{}, k);
-      step(easy, c1, std::false_type{}, k + 1);
+      step(end, c0, std::false_type{}, k);
+      step(end, c1, std::false_type{}, k + 1);
       if constexpr (D > 2) {
-        step(easy, c2, std::false_type{}, k + 2);
-        step(easy, c3, std::false_type{}, k + 3);
+        step(end, c2, std::false_type{}, k + 2);
+        step(end, c3, std::false_type{}, k + 3);
       }
     }
-    std::true_type end;
+    std::true_type last;
     for (; k < steps; k += D) {
-      step(easy, c0, end, k);
-      if (k + 1 < steps) step(easy, c1, end, k + 1);
+      step(end, c0, last, k);
+      if (k + 1 < steps) step(end, c1, last, k + 1);
       if constexpr (D > 2) {
-        if (k + 2 < steps) step(easy, c2, end, k + 2);
-        if (k + 3 < steps) step(easy, c3, end, k + 3);
+        if (k + 2 < steps) step(end, c2, last, k + 2);
+        if (k + 3 < steps) step(end, c3, last, k + 3);
       }
     }
   };
   if (steps > 0) {
     if (p.rows % N == 0 || i0 + BM <= p.rows)
-      run(std::true_type{});
+      run(std::integral_constant<RowEnd, END_WHOLE>{});
+    else if (p.rows >= N)
+      run(std::integral_constant<RowEnd, END_INSIDE>{});
     else
-      run(std::false_type{});
+      run(std::integral_constant<RowEnd, END_SHORT>{});
   }
 
   if (pc.parts == 1 && steps == 0 && p.accumulate) return;
