@@ -352,13 +352,17 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
     q[I] = *reinterpret_cast<const u32x4_t*>(p.x.q + token * p.x.q_pitch + at);
     scale[I] = p.x.scale[token * p.x.s_pitch + at / MUON_CKPT_BLOCK];
   };
+  int by[W];   // elements by which a vector at the row's end was loaded too early
+#pragma unroll
+  for (int i = 0; i < W; ++i) by[i] = max(0, i0 + yc * 8 + i * N - (p.rows - N));
   auto write = [&](auto end, auto slot, int buf, int k0) __attribute__((always_inline)) {
     constexpr int I = decltype(slot)::value;
     LDS_AS char* s = smem + buf * STAGE;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) settle<BF16, decltype(end)::value>(y[I][h][i], i0 + yc * 8 + i * N, p.rows);
+      for (int i = 0; i < W; ++i)
+        if constexpr (decltype(end)::value == END_INSIDE) shift_down<BF16>(y[I][h][i], by[i]);
       if (k0 + yk + 16 * h >= pc.end) {
 #pragma unroll
         for (int i = 0; i < W; ++i) y[I][h][i] = u32x4_t{0, 0, 0, 0};
@@ -512,9 +516,7 @@ __device__ __forceinline__ bf16x8_t frag_x(const LDS_AS char* tile, int kb, int 
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// PARTS == 3: dy in three bf16 parts, a matrix of all tokens each (float32 dy);
-// the parts of 32 tokens are three steps in a row.
-template <int PARTS, int FMT>
+template <int FMT>
 __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
     const WeightGrad p, int tiles_m, int tiles_n) {
   using C = Wide;
@@ -532,8 +534,8 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / C::WGN, wn = wave % C::WGN;
   const int len = pc.end - pc.begin;
-  const int blocks = (len + BK - 1) / BK, steps = blocks * PARTS;
-  const int last = len - (blocks - 1) * BK;   // tokens of the last block
+  const int steps = (len + BK - 1) / BK;
+  const int last = len - (steps - 1) * BK;   // tokens of the last step
 
   // Addresses of this lane's loads within a step.  Columns past a row's end
   // read its last ones instead (they only reach elements of G that are not
@@ -559,27 +561,26 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
   const char* q_base = reinterpret_cast<const char*>(p.x.q) + int64_t(pc.begin) * q_ld;
   const char* s_base = reinterpret_cast<const char*>(p.x.scale) + int64_t(pc.begin) * s_ld;
 
-  auto block_of = [](int k) { return PARTS == 1 ? k : int(uint32_t(k) / PARTS); };
   // Loads of step k: dy into buffer J; the bytes and scales of x to byte `at` of
   // LDS.  END: k may be of
   // the last tokens.
   auto issue_y = [&](auto buf, auto end, int i, int k) {
     constexpr int J = decltype(buf)::value;
     uint32_t off = y_off[i];
-    if (decltype(end)::value && k >= steps - PARTS && y_k[i] >= last)
+    if (decltype(end)::value && k >= steps - 1 && y_k[i] >= last)
       off -= uint32_t(y_k[i] - (last - 1)) * y_ld;
-    dma16(off, y_base + int64_t(block_of(k)) * BK * y_ld + int64_t(k - block_of(k) * PARTS) * p.y_part,
+    dma16(off, y_base + int64_t(k) * BK * y_ld,
           smem_base + J * C::Y_BYTES + (wave * C::Y_INSTR + i) * WAVE_BYTES);
   };
   auto issue_q = [&](auto end, int at, int k) {
     uint32_t off = q_off;
-    if (decltype(end)::value && k >= steps - PARTS && x_k >= last) off -= uint32_t(x_k - (last - 1)) * q_ld;
-    dma16(off, q_base + int64_t(block_of(k)) * BK * q_ld, smem_base + at + wave * WAVE_BYTES);
+    if (decltype(end)::value && k >= steps - 1 && x_k >= last) off -= uint32_t(x_k - (last - 1)) * q_ld;
+    dma16(off, q_base + int64_t(k) * BK * q_ld, smem_base + at + wave * WAVE_BYTES);
   };
   auto issue_s = [&](auto end, int at, int k) {
     uint32_t off = s_off;
-    if (decltype(end)::value && k >= steps - PARTS && x_k >= last) off -= uint32_t(x_k - (last - 1)) * s_ld;
-    dma4(off, s_base + int64_t(block_of(k)) * BK * s_ld, smem_base + at + C::Q_BYTES + wave * 256);
+    if (decltype(end)::value && k >= steps - 1 && x_k >= last) off -= uint32_t(x_k - (last - 1)) * s_ld;
+    dma4(off, s_base + int64_t(k) * BK * s_ld, smem_base + at + C::Q_BYTES + wave * 256);
   };
   // This wave's x bytes of a step, and its part of their bf16 tile X.
   u32x4_t q;
@@ -673,7 +674,7 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
     frags(n, n, 0);
     frags(n, n, 1);
     if (more_x) unpack();
-    if (END && k + 1 < steps && k + 1 >= steps - PARTS && last < BK) zero_tail(buf_1);
+    if (END && k + 1 == steps - 1 && last < BK) zero_tail(buf_1);
     block_barrier();
     multiply(0, 0);
     if (more_y) issue_y(buf_3, end, 0, k + 3);
@@ -731,11 +732,11 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
       unpack();
       write_x(c1);
     }
-    if (steps <= PARTS && last < BK) zero_tail(c0);
+    if (steps == 1 && last < BK) zero_tail(c0);
     block_barrier();
     if (wave >= 4) block_barrier();
     int k = 0;
-    for (; k + 7 + PARTS < steps; k += 4) {   // every load of whole steps
+    for (; k + 8 < steps; k += 4) {   // every load of whole steps
       step(c0, false_type{}, k);
       step(c1, false_type{}, k + 1);
       step(c2, false_type{}, k + 2);
@@ -753,27 +754,17 @@ __global__ __launch_bounds__(64 * Wide::NW, 1) void weight_grad_wide_kernel(
   store_tile<MI>(p, pc, i0 + wm * 128, j0 + wn * 64, acc, smem + wave * kWindow, lane);
 }
 
-// dy as the wide tiles read it: bf16 rows padded with zeros to whole 16-byte
-// vectors; float32 in three parts of 8 bits each (truncation, remainders
-// exact; an infinity leaves no remainder).
-template <bool BF16>
-__global__ __launch_bounds__(kThreads) void repack_kernel(const void* dy, int64_t lddy,
+// dy as the wide tiles read it: rows padded with zeros to whole 16-byte vectors.
+__global__ __launch_bounds__(kThreads) void repack_kernel(const uint16_t* dy, int64_t lddy,
                                                           int64_t tokens, int rows, uint16_t* out,
-                                                          int64_t out_ld, int64_t out_part) {
-  using T = typename RowVec<BF16>::T;
-  constexpr int N = RowVec<BF16>::N, P = BF16 ? 1 : 3;
+                                                          int64_t out_ld) {
   const uint32_t vecs = uint32_t(out_ld / 8);
   const int64_t total = tokens * vecs;
   for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total;
        i += int64_t(gridDim.x) * kThreads) {
     const int64_t t = i / vecs;
     const int col = int(i - t * vecs) * 8;
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += N) load_vec<BF16>(static_cast<const T*>(dy) + t * lddy, col + j, rows, v + j);
-#pragma unroll
-    for (int part = P - 1; part >= 0; --part)   // the smallest part first in memory
-      *reinterpret_cast<u32x4_t*>(out + part * out_part + t * out_ld + col) = take_part(v);
+    *reinterpret_cast<u32x4_t*>(out + t * out_ld + col) = load_raw<true>(dy + t * lddy, col, rows);
   }
 }
 
@@ -829,32 +820,44 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const WeightGrad p, int6
 
 int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
-// Parts that a matrix of `tokens` is cut into, `count` matrices at once: the
-// estimate below at its least.  In microseconds, measured on one MI355X: a
-// round of blocks (one of the 256 x 256 tiles per CU, two of the 128 x 128)
-// takes 6 (start, first loads, stores); a step of 32 tokens 0.6 on a quarter of
-// the CUs and 0.95 on all of them (128 x 128: 0.75, float32 1.2); the partial
-// sums are written at 5 TB/s and joined, through the Infinity Cache, at 10,
-// after 4 (3) for the launch and, for the small matrices, 0.2 per part, each
-// a read that waits for memory.  4096 x 1024 over 16384 tokens: 182 us in 2
-// parts, 131 in 4, 151 in 8; 512 x 512: 83 in 4, 39 in 16, 36 in 32, 46 in 64;
-// 300 x 300 over 300: 18.6 in 1, 12.9 in 3.
-int64_t parts_of(int64_t count, int64_t tokens, int64_t rows, int64_t cols, bool wide, bool bf16) {
+// How a call is cut: its tiles, and the parts of the tokens.
+struct Cut {
+  double us;
+  int64_t parts;
+};
+// The parts that take least, by estimates in microseconds fitted to one MI355X,
+// `count` even matrices at once.  The tiles of 256 x 256 run one to a CU, those
+// of 128 x 128 two; a round of them takes 11 (7) for its start and its stores
+// and, per step of 32 tokens, 0.53 on few CUs to 0.76 on all, where the chip's
+// power and its caches are shared (128 x 128: 0.34 with a CU to itself, 0.59
+// with two on one, a fifth more on rows whose vectors straddle cache lines; float32
+// 0.9 and 1.65).  Partial sums cost 3 for the
+// launch that joins them, 0.25 per part, a read that waits for memory, and 0.8 per
+// 2^20 elements and part to write and read.
+// Estimated against measured: 4096 x 1024 over 16384 tokens, 256 x 256, in 2
+// parts 166 and 167, in 4 127 and 127, in 8 150 and 152; 128 x 128, in 1 part 181
+// and 183, in 4 171 and 175; 256 x 256 over 16384, 128 x 128, in 1 part 182 and
+// 180, in 16 25 and 23.
+Cut cut_of(int64_t count, int64_t tokens, int64_t rows, int64_t cols, bool wide, bool bf16) {
   const int64_t tiles = wide ? cdiv(rows, Wide::BM) * cdiv(cols, Wide::BN) : cdiv(rows, BM) * cdiv(cols, BN);
   const int64_t at_once = wide ? 256 : 512;
-  const double steps = double(cdiv(tokens, BK) * (wide && !bf16 ? 3 : 1));
-  const double g = double(count) * double(rows) * double(cols), join = wide ? 4 : 3;
-  int64_t best = 1;
-  double least = 0;
+  const double g = double(count) * double(rows) * double(cols);
+  auto step = [&](int64_t blocks) {
+    const double u = double(blocks) / 256;
+    if (wide) return 0.53 + 0.23 * u * u * u;
+    if (!bf16) return 0.9 + 0.75 * std::max(0.0, u - 1);
+    return (0.34 + 0.25 * std::max(0.0, u - 1)) * (rows % 8 == 0 ? 1 : 1.2);
+  };
+  Cut best{0, 0};
   for (int64_t n = 1; n <= 64 && n <= cdiv(tokens, 4 * BK); ++n) {
-    const double blocks = double(count * tiles * n), rounds = double(cdiv(count * tiles * n, at_once));
-    const double step = wide ? 0.48 + 0.47 * std::min(1.0, blocks / 256) : bf16 ? 0.75 : 1.2;
-    const double us = rounds * (6 + step * steps / double(n)) + (n > 1 ? join + double(n) * (wide ? 0 : 0.2) + g * double(n) * 12 / 1e7 : 0);
-    if (n == 1 || us < least) {
-      best = n;
-      least = us;
-    }
+    const int64_t blocks = count * tiles * n, rounds = blocks / at_once, rest = blocks % at_once;
+    const double start = wide ? 11 : 7, steps = double(cdiv(cdiv(tokens, n), BK));
+    double us = double(rounds) * (start + step(at_once) * steps);
+    if (rest > 0) us += start + step(rest) * steps;
+    if (n > 1) us += 3 + 0.25 * double(n) + g * double(n) * 0.8e-6;
+    if (n == 1 || us < best.us) best = {us, n};
   }
+  if (best.parts == 0) best.parts = 1;   // no tokens
   return best;
 }
 
@@ -868,18 +871,28 @@ WeightGradPlan weight_grad_plan(int64_t count, int64_t tokens, int64_t rows, int
                                 bool ragged, bool bf16) {
   constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
   WeightGradPlan w{};
-  const int64_t tiles = cdiv(rows, Wide::BM) * cdiv(cols, Wide::BN);
-  // The 256 x 256 tiles need enough work: below four steps per CU the
-  // 128 x 128 tiles, four times as many and quicker to start, are ahead
-  // (768 x 768: 7.4 against 10.3 us over 96 tokens, 15.4 against 18.4 over 512,
-  // 42.2 against 33.9 over 8192).  They read 16-byte rows of bf16: float32 dy
-  // and rows of other lengths are repacked first.
-  w.wide = cdiv(tokens, BK) * tiles * (bf16 ? 1 : 3) >= 4 * 256;
-  if (w.wide && !(bf16 && rows % 8 == 0))
-    w.repack_bytes = size_t(tokens) * size_t(cdiv(rows, 8) * 8) * (bf16 ? 2 : 6);
   const int64_t even = cdiv(tokens, count);
-  int64_t chunk = cdiv(even, parts_of(count, even, rows, cols, w.wide, bf16));
-  if (ragged) chunk = std::max(chunk, tokens / 256 * tiles);
+  Cut cut = cut_of(count, even, rows, cols, false, bf16);
+  // The 256 x 256 tiles are ahead where they fill the chip for many steps
+  // (1024 x 1024: 12.6 against 21.8 us over 700 tokens; 4096 x 1024: 51 against 53
+  // over 4096, 168 against 127 over 16384).  They read rows of whole 16-byte
+  // vectors of bf16; others are repacked first, at 5 TB/s (4095 x 1024 over
+  // 16384: 178 us, 211 with the small tiles).  float32 is bound by its three
+  // products on either, and turned into them in the small tiles.
+  if (bf16) {
+    const Cut c = cut_of(count, even, rows, cols, true, bf16);
+    const bool repack = rows % 8 != 0;
+    w.wide = c.us + (repack ? 3 + double(tokens) * double(rows) * 4 / 5e6 : 0) < cut.us;
+    if (w.wide) {
+      cut = c;
+      if (repack) w.repack_bytes = size_t(tokens) * size_t(cdiv(rows, 8) * 8) * 2;
+    }
+  }
+  int64_t chunk = cdiv(even, cut.parts);
+  if (ragged) {
+    const int64_t tiles = w.wide ? cdiv(rows, Wide::BM) * cdiv(cols, Wide::BN) : cdiv(rows, BM) * cdiv(cols, BN);
+    chunk = std::max(chunk, tokens / (w.wide ? 256 : 512) * tiles);
+  }
   chunk = std::max<int64_t>(4 * BK, cdiv(std::min(chunk, MUON_MAX_TOKENS), BK) * BK);
   w.chunk = uint32_t(chunk);
   if (!ragged) {
@@ -908,14 +921,11 @@ hipError_t launch_small(const WeightGrad& p, dim3 grid, int tm, int tn, hipStrea
     hipLaunchKernelGGL((weight_grad_kernel<BF16, MUON_CKPT_INT8>), grid, dim3(kThreads), 0, s, p, tm, tn);
   return hipGetLastError();
 }
-template <int PARTS>
 hipError_t launch_wide(const WeightGrad& p, dim3 grid, int tm, int tn, hipStream_t s) {
   if (p.x.fmt == MUON_CKPT_E4M3)
-    hipLaunchKernelGGL((weight_grad_wide_kernel<PARTS, MUON_CKPT_E4M3>), grid, dim3(64 * Wide::NW), 0,
-                       s, p, tm, tn);
+    hipLaunchKernelGGL(weight_grad_wide_kernel<MUON_CKPT_E4M3>, grid, dim3(64 * Wide::NW), 0, s, p, tm, tn);
   else
-    hipLaunchKernelGGL((weight_grad_wide_kernel<PARTS, MUON_CKPT_INT8>), grid, dim3(64 * Wide::NW), 0,
-                       s, p, tm, tn);
+    hipLaunchKernelGGL(weight_grad_wide_kernel<MUON_CKPT_INT8>, grid, dim3(64 * Wide::NW), 0, s, p, tm, tn);
   return hipGetLastError();
 }
 
@@ -935,28 +945,22 @@ hipError_t launch_weight_grad(const WeightGrad& call, const WeightGradPlan& plan
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const bool rows16 = p.rows % 8 == 0 && p.lddy % 8 == 0 && reinterpret_cast<uintptr_t>(p.dy) % 16 == 0;
+  const bool rows16 = p.lddy % 8 == 0 && reinterpret_cast<uintptr_t>(p.dy) % 16 == 0;
   if (plan.wide && (plan.repack_bytes > 0 || rows16)) {
     p.y = static_cast<const uint16_t*>(p.dy);
     p.y_ld = p.lddy;
     p.y_cols = p.rows;
-    if (plan.repack_bytes > 0 && !(bf16 && rows16)) {
+    if (plan.repack_bytes > 0) {
       p.y = p.repack;
       p.y_ld = p.y_cols = int(cdiv(p.rows, 8) * 8);
-      p.y_part = p.tokens * p.y_ld * 2;
       const int64_t blocks = cdiv(p.tokens * (p.y_ld / 8), kThreads);
-      const dim3 g(unsigned(std::min<int64_t>(blocks, 16384)));
-      if (bf16)
-        hipLaunchKernelGGL(repack_kernel<true>, g, dim3(kThreads), 0, s, p.dy, p.lddy, p.tokens,
-                           p.rows, p.repack, p.y_ld, p.y_part / 2);
-      else
-        hipLaunchKernelGGL(repack_kernel<false>, g, dim3(kThreads), 0, s, p.dy, p.lddy, p.tokens,
-                           p.rows, p.repack, p.y_ld, p.y_part / 2);
+      hipLaunchKernelGGL(repack_kernel, dim3(unsigned(std::min<int64_t>(blocks, 16384))), dim3(kThreads), 0,
+                         s, static_cast<const uint16_t*>(p.dy), p.lddy, p.tokens, p.rows, p.repack, p.y_ld);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
     const int tm = int(cdiv(p.rows, Wide::BM)), tn = int(cdiv(p.cols, Wide::BN));
-    return bf16 ? launch_wide<1>(p, grid(tm, tn), tm, tn, s) : launch_wide<3>(p, grid(tm, tn), tm, tn, s);
+    return launch_wide(p, grid(tm, tn), tm, tn, s);
   }
   const int tm = int(cdiv(p.rows, BM)), tn = int(cdiv(p.cols, BN));
   return bf16 ? launch_small<true>(p, grid(tm, tn), tm, tn, s) : launch_small<false>(p, grid(tm, tn), tm, tn, s);

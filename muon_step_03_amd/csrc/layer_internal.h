@@ -129,11 +129,9 @@ __device__ __forceinline__ u32x4_t load_ahead(const void* row, int col, int cols
       *reinterpret_cast<const typename R::Raw*>(static_cast<const typename R::T*>(row) + at);
   return u32x4_t{r[0], r[1], r[2], r[3]};
 }
-template <bool BF16, RowEnd END>
-__device__ __forceinline__ void settle(u32x4_t& w, int col, int cols) {
-  if constexpr (END != END_INSIDE) return;
-  int by = col - (cols - RowVec<BF16>::N);   // elements
-  if (by <= 0) return;
+// A vector without its first `by` elements, zeros behind the last.
+template <bool BF16>
+__device__ __forceinline__ void shift_down(u32x4_t& w, int by) {
   if constexpr (BF16) {
     if (by & 1)
       w = u32x4_t{w[0] >> 16 | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | w[3] << 16, w[3] >> 16};
@@ -142,6 +140,12 @@ __device__ __forceinline__ void settle(u32x4_t& w, int col, int cols) {
   if (by & 1) w = u32x4_t{w[1], w[2], w[3], 0};
   if (by & 2) w = u32x4_t{w[2], w[3], 0, 0};
   if (by >= 4) w = u32x4_t{0, 0, 0, 0};
+}
+template <bool BF16, RowEnd END>
+__device__ __forceinline__ void settle(u32x4_t& w, int col, int cols) {
+  if constexpr (END != END_INSIDE) return;
+  const int by = col - (cols - RowVec<BF16>::N);
+  if (by > 0) shift_down<BF16>(w, by);
 }
 template <bool BF16>
 __device__ __forceinline__ void unpack_raw(u32x4_t w, float* v) {
@@ -401,11 +405,10 @@ struct WeightGrad {
   uint32_t chunk;
   int64_t pieces;          // upper bound over all matrices
   void* table;             // with offsets: the pieces and the split matrices
-  uint16_t* repack;        // workspace for dy in aligned bf16 rows
+  uint16_t* repack;        // workspace for dy in aligned rows
   // dy as the 256 x 256 tiles read it
   const uint16_t* y;
   int64_t y_ld;            // elements
-  int64_t y_part;          // bytes between the parts of float32 dy
   int y_cols;              // columns that may be read
 };
 // The cut of the tokens, which also sizes the workspace: partial sums, then
