@@ -281,20 +281,18 @@ __device__ __forceinline__ void unpack4(uint32_t q, int byte, uint32_t& lo, uint
   }
 }
 
-// The leading 8 bits of each of 8 values as bf16, which are taken off them: three
-// calls give all 24 bits of float32 values.  An infinity leaves no remainder.
-__device__ __forceinline__ u32x4_t take_part(float (&v)[8]) {
-  u32x4_t w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = __float_as_uint(v[2 * i]) & 0xffff0000u;
-    const uint32_t b = __float_as_uint(v[2 * i + 1]) & 0xffff0000u;
-    w[i] = (a >> 16) | b;
-    const float fa = __uint_as_float(a), fb = __uint_as_float(b);
-    v[2 * i] = v[2 * i] == fa ? 0.f : v[2 * i] - fa;
-    v[2 * i + 1] = v[2 * i + 1] == fb ? 0.f : v[2 * i + 1] - fb;
-  }
-  return w;
+// Two float32 values as three bf16 pairs that add up to them exactly.  The
+// first is cut off, for a value near the largest must not become an infinity
+// (which itself leaves no remainder); 16 bits remain, whose half is rounded off
+// and leaves 8.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&o)[3]) {
+  const uint32_t a = __float_as_uint(x) & 0xffff0000u, b = __float_as_uint(y) & 0xffff0000u;
+  o[0] = (a >> 16) | b;
+  const float fa = __uint_as_float(a), fb = __uint_as_float(b);
+  x = x == fa ? 0.f : x - fa;
+  y = y == fb ? 0.f : y - fb;
+  o[1] = f2bf2(x, y);
+  o[2] = f2bf2(x - __uint_as_float(o[1] << 16), y - __uint_as_float(o[1] & 0xffff0000u));
 }
 
 // Byte address of the 8 columns `chunk` of token row k in a [BK][128] tile.
@@ -373,9 +371,13 @@ __global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(const WeightGr
         float v[8];
 #pragma unroll
         for (int i = 0; i < W; ++i) unpack_raw<false>(y[I][h][i], v + i * N);
+        uint32_t o[4][3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split3(v[2 * i], v[2 * i + 1], o[i]);
 #pragma unroll
         for (int part = 0; part < P; ++part)
-          *reinterpret_cast<LDS_AS u32x4_t*>(s + part * PLANE + tile_at(yk + 16 * h, yc)) = take_part(v);
+          *reinterpret_cast<LDS_AS u32x4_t*>(s + part * PLANE + tile_at(yk + 16 * h, yc)) =
+              u32x4_t{o[0][part], o[1][part], o[2][part], o[3][part]};
       }
     }
     uint32_t o[8];
@@ -829,11 +831,11 @@ struct Cut {
 // `count` even matrices at once.  The tiles of 256 x 256 run one to a CU, those
 // of 128 x 128 two; a round of them takes 11 (7) for its start and its stores
 // and, per step of 32 tokens, 0.53 on few CUs to 0.76 on all, where the chip's
-// power and its caches are shared (128 x 128: 0.34 with a CU to itself, 0.59
-// with two on one, a fifth more on rows whose vectors straddle cache lines; float32
-// 0.9 and 1.65).  Partial sums cost 3 for the
-// launch that joins them, 0.25 per part, a read that waits for memory, and 0.8 per
-// 2^20 elements and part to write and read.
+// power and its caches are shared (128 x 128: 0.34 where each has a CU to itself,
+// 0.59 where some have not, a fifth more on rows whose vectors straddle cache
+// lines; float32 0.87 and 1.6).  Partial sums cost 3 for the launch that joins
+// them, 0.25 per part, a read that waits for memory, and 0.8 per 2^20 elements
+// and part to write and read.
 // Estimated against measured: 4096 x 1024 over 16384 tokens, 256 x 256, in 2
 // parts 166 and 167, in 4 127 and 127, in 8 150 and 152; 128 x 128, in 1 part 181
 // and 183, in 4 171 and 175; 256 x 256 over 16384, 128 x 128, in 1 part 182 and
@@ -845,8 +847,8 @@ Cut cut_of(int64_t count, int64_t tokens, int64_t rows, int64_t cols, bool wide,
   auto step = [&](int64_t blocks) {
     const double u = double(blocks) / 256;
     if (wide) return 0.53 + 0.23 * u * u * u;
-    if (!bf16) return 0.9 + 0.75 * std::max(0.0, u - 1);
-    return (0.34 + 0.25 * std::max(0.0, u - 1)) * (rows % 8 == 0 ? 1 : 1.2);
+    if (!bf16) return u > 1 ? 1.6 : 0.87;
+    return (u > 1 ? 0.59 : 0.34) * (rows % 8 == 0 ? 1 : 1.2);
   };
   Cut best{0, 0};
   for (int64_t n = 1; n <= 64 && n <= cdiv(tokens, 4 * BK); ++n) {
