@@ -369,6 +369,94 @@ def test_weight_grad_float32_infinity():
     assert not bool(G[[0, 1, 3, 5, 6, 7]].any())
 
 
+# Sizes whose estimated times choose the 256 x 256 tiles: whole rows, and odd
+# ones, which are repacked; matrices in one part and in several.
+LARGE = [(640, 4096, 2056), (2100, 2056, 2050), (2100, 2051, 2050), (5003, 2056, 1030)]
+
+
+@pytest.mark.parametrize("tokens,rows,cols", LARGE)
+@pytest.mark.parametrize("gdtype,fmt", [(BF16, "int8"), (F32, "e4m3")])
+def test_weight_grad_large(tokens, rows, cols, gdtype, fmt):
+    dy, ck, x64 = weight_case(tokens, rows, cols, BF16, fmt, seed=rows)
+    into = params(rows * cols, gdtype, seed=3)[0].view(rows, cols)
+    before = into.clone()
+    check_weight(M.weight_grad(dy, ck, dtype=gdtype), dy, x64)
+    check_weight(M.weight_grad(dy, ck, G=into, accumulate=True), dy, x64, before=before)
+
+
+COUNTS = [0, 1, 31, 32, 33, 2000, 64, 0, 3839, 1000, 700, 1300]
+
+
+@pytest.mark.parametrize("rows", [776, 771])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_weight_grad_large_ragged(rows, fmt):
+    dy, ck, x64 = weight_case(9003, rows, 1030, BF16, fmt, seed=rows)
+    off = offsets_of(COUNTS)
+    G = M.weight_grad(dy, ck, offsets=off.to(DEV))
+    check_weight(G, dy, x64, off.tolist())
+    assert not G[[0, 7]].any()
+    before = torch.randn(G.shape, generator=torch.Generator().manual_seed(1)).to(BF16).to(DEV) * 1e-2
+    into = before.clone()
+    M.weight_grad(dy, ck, offsets=off.to(DEV), G=into, accumulate=True)
+    check_weight(into, dy, x64, off.tolist(), before)
+    # tokens of one matrix that are NaN, in steps that its neighbours share
+    dy[off[5] - 1] = float("nan")
+    again = M.weight_grad(dy, ck, offsets=off.to(DEV))
+    assert bool(again[4].isnan().all())
+    others = [i for i in range(12) if i != 4]
+    assert torch.equal(again[others], G[others])
+    bad = torch.tensor([-7, 0, 10 ** 12] + [5] * 9 + [-1], dtype=torch.int64, device=DEV)
+    dy[off[5] - 1] = 0.0
+    got = M.weight_grad(dy, ck, offsets=bad)
+    check_weight(got[1:2], dy, x64, [0, 9003])
+    assert not got[[0, *range(2, 12)]].any()
+
+
+@pytest.mark.parametrize("rows", [2056, 2051])
+def test_weight_grad_large_exact_integers(rows):
+    tokens, cols = 2100, 2050
+    g = torch.Generator().manual_seed(rows)
+    x = torch.randint(-1, 2, (tokens, cols), generator=g).to(BF16).to(DEV)
+    dy = torch.randint(-128, 129, (tokens, rows), generator=g).to(BF16).to(DEV)
+    want = dy.cpu().double().t() @ x.cpu().double()
+    wide = torch.full((tokens, rows + 24), float("nan"), dtype=BF16, device=DEV)
+    for fmt in FMTS:
+        ck = M.checkpoint_save(x, fmt)
+        assert torch.equal(M.weight_grad(dy, ck, dtype=F32).cpu().double(), want)
+        for start in (8, 3):      # rows that start on 16 bytes, and rows that do not
+            view = wide[:, start:start + rows]
+            view.copy_(dy)
+            assert torch.equal(M.weight_grad(view, ck, dtype=F32).cpu().double(), want)
+            wide.fill_(float("nan"))
+
+
+# Rows that end inside a vector, before its end, or with it.
+@pytest.mark.parametrize("cols", [2, 3, 5, 6, 7, 9, 11, 12, 15, 250, 509, 1027])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_row_ends(cols, dtype):
+    tokens = 37
+    x, dy = hidden(tokens, cols, dtype, seed=cols), grads(tokens, cols, dtype, seed=cols)
+    gain, bias = params(cols, dtype)
+    out = M.layernorm_forward(x, gain, bias, x_checkpoint="int8", y_checkpoint="e4m3")
+    check_forward(out, x, gain, bias, 1e-5)
+    check_checkpoint(out.x_checkpoint, f64(x), "int8")
+    check_checkpoint(out.y_checkpoint, f64(out.y), "e4m3")
+    check_backward(M.layernorm_backward(dy, x, gain, out.mean, out.rstd), dy, f64(x), gain,
+                   out.mean, out.rstd)
+    check_weight(M.weight_grad(dy, out.x_checkpoint), dy, f64(M.checkpoint_restore(out.x_checkpoint, F32)))
+    # the same rows with others' bytes on both sides: nothing of them gets in
+    w = torch.full((tokens, cols + 9), float("nan"), dtype=dtype, device=DEV)
+    dw = w.clone()
+    w[:, 4:4 + cols], dw[:, 5:5 + cols] = x, dy
+    at = M.layernorm_forward(w[:, 4:4 + cols], gain, bias, x_checkpoint="int8")
+    assert torch.equal(at.y, out.y) and torch.equal(at.x_checkpoint.q, out.x_checkpoint.q)
+    for a, b in zip(M.layernorm_backward(dw[:, 5:5 + cols], w[:, 4:4 + cols], gain, out.mean, out.rstd),
+                    M.layernorm_backward(dy, x, gain, out.mean, out.rstd)):
+        assert torch.equal(a, b)
+    assert torch.equal(M.weight_grad(dw[:, 5:5 + cols], out.x_checkpoint),
+                       M.weight_grad(dy, out.x_checkpoint))
+
+
 # ----------------------------------------------------- how calls are made
 def test_same_bits_every_time_and_given_buffers():
     x, dy = hidden(3000, 520, BF16, seed=2), grads(3000, 520, BF16, seed=2)
