@@ -1,7 +1,8 @@
 // Activation checkpoints: x -> 8-bit q with one power-of-two scale per block of
 // 32 columns, and back.  HBM-bound: 2 (or 4) bytes in and 33/32 out per
 // element, and the reverse.  32768 x 4096 bf16 to e4m3 on one MI355X: 84 us
-// (4.8 TB/s), back 70 (5.8; a 1 GiB copy moves 5.45).
+// (4.8 TB/s; 69 and 5.9 after a restore has left the caches alone), back 62 (6.6; a
+// 1 GiB copy moves 5.45).
 //
 // A vector is 16 bytes of x (8 bf16 or 4 float32), so 4 or 8 consecutive lanes
 // hold a block and find its largest magnitude with two or three lane exchanges.
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(kThreads) void save_kernel(const void* x, int64_t l
   }
 }
 
-template <bool BF16>
+template <bool BF16, bool STREAM>
 __global__ __launch_bounds__(kThreads) void restore_kernel(Ckpt c, void* x, int64_t tokens,
                                                            int cols) {
   using R = RowVec<BF16>;
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void restore_kernel(Ckpt c, void* x, int6
       if (row[j] < tokens) {
         float v[N];
         ckpt_values<N>(r8[j], c.fmt, v);
-        store_vec<BF16>(static_cast<typename R::T*>(x) + row[j] * cols, col[j], cols, v);
+        store_vec<BF16, STREAM>(static_cast<typename R::T*>(x) + row[j] * cols, col[j], cols, v);
       }
   }
 }
@@ -107,12 +108,19 @@ hipError_t launch_ckpt_restore(const Ckpt& c, void* x, bool bf16, int64_t tokens
                                hipStream_t s) {
   const int n = bf16 ? 8 : 4;
   const int64_t vecs = tokens * int64_t((cols + n - 1) / n);
-  if (bf16)
-    hipLaunchKernelGGL(restore_kernel<true>, dim3(grid_for(vecs)), dim3(kThreads), 0, s, c, x,
-                       tokens, cols);
+  // More than half of the 256 MB Infinity Cache streams past it: save and restore
+  // of 32768 x 4096 bf16 156 -> 131 us, with a reader of the values 164 -> 152;
+  // for 16384 x 4096 the reader loses more than the 8 us that the restore gains.
+  const bool stream = tokens * int64_t(cols) * (bf16 ? 2 : 4) > (int64_t(1) << 27);
+  const dim3 grid(grid_for(vecs)), block(kThreads);
+  if (bf16 && stream)
+    hipLaunchKernelGGL((restore_kernel<true, true>), grid, block, 0, s, c, x, tokens, cols);
+  else if (bf16)
+    hipLaunchKernelGGL((restore_kernel<true, false>), grid, block, 0, s, c, x, tokens, cols);
+  else if (stream)
+    hipLaunchKernelGGL((restore_kernel<false, true>), grid, block, 0, s, c, x, tokens, cols);
   else
-    hipLaunchKernelGGL(restore_kernel<false>, dim3(grid_for(vecs)), dim3(kThreads), 0, s, c, x,
-                       tokens, cols);
+    hipLaunchKernelGGL((restore_kernel<false, false>), grid, block, 0, s, c, x, tokens, cols);
   return hipGetLastError();
 }
 

@@ -195,7 +195,10 @@ __device__ __forceinline__ void place_tile(int tile, int tiles_m, int tiles_n, i
 }
 
 // Eight consecutive columns of one row: into the gradient, or (to != null)
-// into a row-major float32 matrix of partial sums.
+// into a row-major float32 matrix of partial sums.  A bf16 gradient streams past
+// the caches (64 even experts of 1408 x 512 over 49152 tokens: 89 -> 82 us;
+// float32, whose rows are stored in halves, 112 -> 119); the join finds the
+// partial sums there.
 __device__ __forceinline__ void store_row8(const WeightGrad& p, float* to, int64_t base, int row,
                                            int col, f32x4_t lo, f32x4_t hi) {
   if (row >= p.rows || col >= p.cols) return;
@@ -220,7 +223,7 @@ __device__ __forceinline__ void store_row8(const WeightGrad& p, float* to, int64
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += old[i];
     }
-    store_vec<true>(g, 0, left, v);
+    store_vec<true, true>(g, 0, left, v);
   } else {
     float* g = static_cast<float*>(p.G) + base + at;
     if (p.accumulate) {

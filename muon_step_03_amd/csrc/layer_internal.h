@@ -166,13 +166,18 @@ __device__ __forceinline__ u32x4_t pack_raw(const float* v) {
   for (int i = 0; i < 4; ++i) w[i] = BF16 ? f2bf2(v[2 * i], v[2 * i + 1]) : __float_as_uint(v[i]);
   return w;
 }
-template <bool BF16, bool EVEN = false>
+// STREAM: the caches need not keep it.
+template <bool BF16, bool EVEN = false, bool STREAM = false>
 __device__ __forceinline__ void store_raw(void* row, int col, int cols, u32x4_t w) {
   using R = RowVec<BF16>;
   using T = typename R::T;
   T* p = static_cast<T*>(row) + col;
   if (col + R::N <= cols) {
-    *reinterpret_cast<typename R::Raw*>(p) = typename R::Raw{w[0], w[1], w[2], w[3]};
+    const typename R::Raw r = {w[0], w[1], w[2], w[3]};
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(r, reinterpret_cast<typename R::Raw*>(p));
+    else
+      *reinterpret_cast<typename R::Raw*>(p) = r;
   } else if constexpr (!EVEN) {
 #pragma unroll
     for (int i = 0; i < R::N; ++i)
@@ -210,9 +215,9 @@ __device__ __forceinline__ void load_params(const void* base, bool bf16, int col
   }
 }
 
-template <bool BF16>
+template <bool BF16, bool STREAM = false>
 __device__ __forceinline__ void store_vec(void* row, int col, int cols, const float* v) {
-  store_raw<BF16>(row, col, cols, pack_raw<BF16>(v));
+  store_raw<BF16, false, STREAM>(row, col, cols, pack_raw<BF16>(v));
 }
 
 // Lane exchanges within a row of 16 lanes (data-parallel-primitive moves).

@@ -69,6 +69,16 @@ def test_checkpoint_strided_odd_start_and_out():
     assert np.array_equal(f64(into), values)
 
 
+@pytest.mark.parametrize("dtype,cols", [(BF16, 2000), (F32, 1000), (F32, 1001)])
+def test_checkpoint_larger_than_the_caches(dtype, cols):
+    x = hidden(500, cols, dtype).repeat(80, 1)      # over 2^27 bytes
+    assert x.numel() * x.element_size() > 2 ** 27
+    ck = M.checkpoint_save(x, "int8")
+    near = M.checkpoint_restore(M.checkpoint_save(x[:500], "int8"), dtype)
+    assert torch.equal(M.checkpoint_restore(ck, dtype).view(80, 500, cols),
+                       near.expand(80, 500, cols))
+
+
 def test_checkpoint_no_tokens():
     ck = M.checkpoint_save(torch.empty(0, 70, dtype=BF16, device=DEV))
     assert ck.shape == (0, 70) and M.checkpoint_restore(ck).shape == (0, 70)
