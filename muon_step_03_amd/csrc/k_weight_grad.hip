@@ -194,15 +194,13 @@ __device__ __forceinline__ void place_tile(int tile, int tiles_m, int tiles_n, i
   ti = group * 8 + r - tj * rows;
 }
 
-// Eight consecutive columns of one row: into the gradient, or (to != null)
-// into a row-major float32 matrix of partial sums.  A bf16 gradient streams past
-// the caches (64 even experts of 1408 x 512 over 49152 tokens: 89 -> 82 us;
-// float32, whose rows are stored in halves, 112 -> 119); the join finds the
-// partial sums there.
-__device__ __forceinline__ void store_row8(const WeightGrad& p, float* to, int64_t base, int row,
-                                           int col, f32x4_t lo, f32x4_t hi) {
+// Eight consecutive columns of one row into a bf16 gradient.  The L2 need not
+// keep what is stored (64 even experts of 1408 x 512 over 49152 tokens: 89 -> 82
+// us; float32 over 16384: 117 -> 113): the join's reads of partial sums come from
+// the Infinity Cache all the same (1001 x 777 over 2049: 29.9 -> 28.5).
+__device__ __forceinline__ void store_bf16(const WeightGrad& p, int64_t base, int row, int col,
+                                           f32x4_t lo, f32x4_t hi) {
   if (row >= p.rows || col >= p.cols) return;
-  const int64_t at = int64_t(row) * p.cols + col;
   float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -210,31 +208,29 @@ __device__ __forceinline__ void store_row8(const WeightGrad& p, float* to, int64
     v[4 + i] = hi[i];
   }
   const int left = p.cols - col;
-  if (to) {
-    store_vec<false>(to + at, 0, left, v);
-    store_vec<false>(to + at, 4, left, v + 4);
-    return;
-  }
-  float old[8];
-  if (p.g_bf16) {
-    uint16_t* g = static_cast<uint16_t*>(p.G) + base + at;
-    if (p.accumulate) {
-      load_vec<true>(g, 0, left, old);
+  uint16_t* g = static_cast<uint16_t*>(p.G) + base + int64_t(row) * p.cols + col;
+  if (p.accumulate) {
+    float old[8];
+    load_vec<true>(g, 0, left, old);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += old[i];
-    }
-    store_vec<true, true>(g, 0, left, v);
-  } else {
-    float* g = static_cast<float*>(p.G) + base + at;
-    if (p.accumulate) {
-      load_vec<false>(g, 0, left, old);
-      load_vec<false>(g, 4, left, old + 4);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += old[i];
-    }
-    store_vec<false>(g, 0, left, v);
-    store_vec<false>(g, 4, left, v + 4);
+    for (int i = 0; i < 8; ++i) v[i] += old[i];
   }
+  store_vec<true, true>(g, 0, left, v);
+}
+// Four into a float32 matrix: the gradient, or a piece's partial sums.
+__device__ __forceinline__ void store_f32(const WeightGrad& p, float* to, bool add, int row, int col,
+                                          f32x4_t x) {
+  if (row >= p.rows || col >= p.cols) return;
+  float v[4] = {x[0], x[1], x[2], x[3]};
+  const int left = p.cols - col;
+  to += int64_t(row) * p.cols + col;
+  if (add) {
+    float old[4];
+    load_vec<false>(to, 0, left, old);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += old[i];
+  }
+  store_vec<false, true>(to, 0, left, v);
 }
 
 // Writes a wave's 32 MI x 64 accumulators (rows from i0, columns from j0)
@@ -248,7 +244,8 @@ __device__ __forceinline__ void store_tile(const WeightGrad& p, const Piece& pc,
                                            const f32x16_t (&acc)[MI][2], LDS_AS char* window,
                                            int lane) {
   const int64_t size = int64_t(p.rows) * p.cols;
-  float* to = pc.parts > 1 ? p.partial + pc.slot * size : nullptr;
+  const bool whole = pc.parts == 1, f32 = !whole || !p.g_bf16;
+  float* to = whole ? static_cast<float*>(p.G) + pc.e * size : p.partial + pc.slot * size;   // f32
   LDS_AS float* w = (LDS_AS float*)window;
 #pragma unroll
   for (int a = 0; a < MI; ++a) {
@@ -260,12 +257,21 @@ __device__ __forceinline__ void store_tile(const WeightGrad& p, const Piece& pc,
             f32x4_t{acc[a][b][4 * g], acc[a][b][4 * g + 1], acc[a][b][4 * g + 2],
                     acc[a][b][4 * g + 3]};
     wave_lds_sync();
+    if (f32) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = r * 8 + (lane >> 3), col = (lane & 7) * 8;
-      const f32x4_t lo = *(const LDS_AS f32x4_t*)(w + row * 68 + col);
-      const f32x4_t hi = *(const LDS_AS f32x4_t*)(w + row * 68 + col + 4);
-      store_row8(p, to, pc.e * size, i0 + a * 32 + row, j0 + col, lo, hi);
+      for (int r = 0; r < 8; ++r) {
+        const int row = r * 4 + (lane >> 4), col = (lane & 15) * 4;
+        store_f32(p, to, whole && p.accumulate, i0 + a * 32 + row, j0 + col,
+                  *(const LDS_AS f32x4_t*)(w + row * 68 + col));
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = r * 8 + (lane >> 3), col = (lane & 7) * 8;
+        store_bf16(p, pc.e * size, i0 + a * 32 + row, j0 + col,
+                   *(const LDS_AS f32x4_t*)(w + row * 68 + col),
+                   *(const LDS_AS f32x4_t*)(w + row * 68 + col + 4));
+      }
     }
     wave_lds_sync();
   }
