@@ -42,17 +42,19 @@ __device__ __forceinline__ void wait_vmcnt() {
 // aliasing it (which would make it wait for all loads in flight, prefetches
 // included); completion is tracked explicitly with wait_vmcnt before the
 // barrier that publishes a K step.  The instruction has no result register.
+// It reads m0 one wait state after a scalar write at the earliest, which only the
+// compiler's own instructions are spaced for: s_nop.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(uint32_t off, const char* base, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
                : "v"(off), "s"(base), "s"(lds_base)
                : "memory", "m0");
 }
 // The same for 4 bytes per lane.
 __device__ __forceinline__ void dma4(uint32_t off, const char* base, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                :
                : "v"(off), "s"(base), "s"(lds_base)
                : "memory", "m0");
