@@ -286,12 +286,10 @@ __device__ __forceinline__ void unpack4(uint32_t q, int byte, uint32_t& lo, uint
     lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, up, false));
     hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, up, true));
   } else {
-    // bytes offset to unsigned, the offset taken off again in the scaling
-    const float up = ckpt_up(byte), off = -128.f * up;
-    const uint32_t w = q ^ 0x80808080u;
+    // each byte is converted with its sign before it is scaled: at the largest
+    // scales an offset times 2^e would be infinite where the values are not
     float v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(float((w >> (8 * j)) & 0xffu), up, off);
+    ckpt_unpack4(q, ckpt_up(byte), FMT, v);
     lo = f2bf2(v[0], v[1]);
     hi = f2bf2(v[2], v[3]);
   }
