@@ -64,10 +64,12 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* red) {
   }
 }
 
-// s / n with inv = 1 / n rounded: the quotient is corrected by its remainder.
+// s / n with inv = 1 / n rounded: the quotient is corrected by its remainder,
+// which an infinite one does not have.
 __device__ __forceinline__ float over(float s, float n, float inv) {
   const float q = s * inv;
-  return __builtin_fmaf(__builtin_fmaf(-q, n, s), inv, q);
+  const float c = __builtin_fmaf(__builtin_fmaf(-q, n, s), inv, q);
+  return __builtin_fabsf(q) < __builtin_inff() ? c : q;
 }
 
 // 1 / sqrt(v) within half a step and a little: the hardware's estimate (one
