@@ -13,6 +13,7 @@ alive, as for any PyTorch layer.
 """
 from __future__ import annotations
 
+import math
 from typing import Optional, Union
 
 import torch
@@ -71,12 +72,20 @@ def layer_norm(x, gain, bias=None, *, eps=1e-5, keep: Optional[str] = None,
     return y if y_keep is None else (y, ActCheckpoint(q, scale, x.shape[-1]))
 
 
+def _product(x, B):
+    """x [..., n] times a matrix B: one product of two matrices.  (``x @ B`` is
+    one over batches, each with an expanded B, where x's leading dimensions do
+    not fold.)"""
+    with torch.autocast(device_type=x.device.type, enabled=False):
+        rows = x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
+        return (rows @ B).view(*x.shape[:-1], B.shape[1])
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, q, scale):
         ctx.save_for_backward(W, q, scale)
-        with torch.autocast(device_type=x.device.type, enabled=False):
-            return x @ W.t()
+        return _product(x, W.t())
 
     @staticmethod
     @once_differentiable
@@ -84,8 +93,7 @@ class _Linear(torch.autograd.Function):
         W, q, scale = ctx.saved_tensors
         dx = dW = None
         if ctx.needs_input_grad[0]:
-            with torch.autocast(device_type=dy.device.type, enabled=False):
-                dx = dy @ W
+            dx = _product(dy, W)
         if ctx.needs_input_grad[1]:
             dW = weight_grad(_rows(dy), ActCheckpoint(q, scale, W.shape[1]), dtype=W.dtype)
         return dx, dW, None, None
@@ -102,8 +110,7 @@ def linear(x, W, keep: Union[str, ActCheckpoint] = "e4m3"):
     if x.shape[-1] != W.shape[1]:
         raise ValueError(f"x has {x.shape[-1]} columns, W {W.shape[1]}")
     if not (torch.is_grad_enabled() and W.requires_grad):
-        with torch.autocast(device_type=x.device.type, enabled=False):
-            return x @ W.t()      # no weight gradient: nothing is kept
+        return _product(x, W.t())      # no weight gradient: nothing is kept
     if isinstance(keep, ActCheckpoint):
         if keep.shape != (x.numel() // max(1, x.shape[-1]), x.shape[-1]) or keep.device != x.device:
             raise ValueError(f"keep is {keep}, x has shape {tuple(x.shape)} on {x.device}")

@@ -210,3 +210,26 @@ def test_captured_training_pass():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, held))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("layout", ["transposed", "sliced", "columns"])
+def test_linear_of_inputs_that_do_not_fold(dtype, layout):
+    """Sequences read across, a slice of longer ones, columns outermost: the
+    same values and gradients as of a contiguous copy."""
+    base = hidden(84, 136, dtype, seed=2)
+    x = {"transposed": base[:42].view(21, 2, 136).transpose(0, 1),
+         "sliced": base.view(2, 42, 136)[:, 3:24],
+         "columns": base[:42].t().contiguous().t().view(2, 21, 136)}[layout]
+    assert not x.is_contiguous()
+    W = hidden(72, 136, dtype, seed=3, scale=0.05)
+    dz = grads(42, 72, dtype, seed=2).view(21, 2, 72).transpose(0, 1)
+    got, want = [], []
+    for a, b, to in ((x, dz, got), (x.contiguous(), dz.contiguous(), want)):
+        X, V = a.detach().requires_grad_(), leaf(W)
+        z = M.linear(X, V)
+        to += [z.detach(), *torch.autograd.grad(z, (X, V), b)]
+        z = M.linear(X, W)      # W frozen
+        to += [z.detach(), *torch.autograd.grad(z, X, b)]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    check_weight(got[2], dz.reshape(42, 72), lo.checkpoint(f64(x.reshape(42, 136)), "e4m3")[0])
