@@ -28,8 +28,14 @@ _FORMAT_CODES = {torch.float8_e4m3fn: _lib.MUON_CKPT_E4M3, torch.int8: _lib.MUON
 _FORMAT_NAMES = {v: k for k, v in FORMATS.items()}
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle, no object
-_current_device = torch._C._cuda_getDevice
+# Looked up at the call: a PyTorch without a GPU backend does not have them.
+def _raw_stream(index):
+    """The current stream's handle, with no stream object made."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _current_device():
+    return torch._C._cuda_getDevice()
 
 
 def _away(t, stream) -> bool:
