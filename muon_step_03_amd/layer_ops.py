@@ -156,6 +156,8 @@ class ActCheckpoint:
         ck = cls.__new__(cls)
         ck._buffer = torch.empty(size + tokens * ((cols + 127) // 128 * 4), dtype=torch.uint8,
                                  device=device)
+        if not ck._buffer.is_cuda:
+            raise ValueError(f"a checkpoint must be on a GPU, not on {ck._buffer.device}")
         ck._q = ck._scale = None
         ck._shape, ck._store = (tokens, cols), store
         at = ck._buffer.data_ptr()

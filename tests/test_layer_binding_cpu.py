@@ -3,6 +3,10 @@ import os
 import subprocess
 import sys
 
+import pytest
+
+import muon_step_03_amd as M
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -23,3 +27,11 @@ def test_import_without_the_gpu_parts_of_pytorch():
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "REFUSED" in r.stdout
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+def test_checkpoints_are_on_a_gpu(device):
+    """An unwritten checkpoint elsewhere is refused when it is made, like one of
+    given tensors."""
+    with pytest.raises(ValueError, match="must be on a GPU"):
+        M.ActCheckpoint.empty(4, 64, device=device)
