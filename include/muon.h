@@ -364,7 +364,9 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
  * buffers; tokens before the first or from the last offset on belong to no
  * matrix.  A matrix without tokens gets zeros.  accumulate != 0 adds to what G
  * holds.  Products are exact in float32 (float32 dy is taken in three bf16
- * parts, which hold its 24 bits) and accumulate in float32; G is rounded once.
+ * parts, which hold its 24 bits down to 2^-133: of an element below 2^-109 in
+ * magnitude at most 2^-134 is rounded off) and accumulate in float32; G is
+ * rounded once.
  */
 #define MUON_WEIGHT_GRAD_MAX_COUNT (1 << 20)
 size_t muon_weight_grad_workspace_bytes(int64_t count, int with_offsets, int64_t tokens,

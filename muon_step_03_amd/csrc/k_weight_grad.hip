@@ -7,7 +7,7 @@
 // LDS reads.  x is brought back from 8 bits when it is written to LDS: a
 // checkpoint's values are exact in bf16, so bf16 matrix cores see exactly what
 // it holds.  float32 dy is split into three bf16 parts of 8 bits each
-// (remainders exact), whose three products per element replace the sixteen
+// (remainders exact, see split3), whose three products per element replace the sixteen
 // times slower float32 matrix instruction.
 //
 // Bound by the matrix cores for many tokens (an element of G takes 2 flops per
@@ -295,10 +295,11 @@ __device__ __forceinline__ void unpack4(uint32_t q, int byte, uint32_t& lo, uint
   }
 }
 
-// Two float32 values as three bf16 pairs that add up to them exactly.  The
-// first is cut off, for a value near the largest must not become an infinity
-// (which itself leaves no remainder); 16 bits remain, whose half is rounded off
-// and leaves 8.
+// Two float32 values as three bf16 pairs that add up to them exactly, down to
+// bf16's smallest step of 2^-133 (the 24 bits of a value below 2^-109 reach further
+// down: at most 2^-134 of it is rounded off).  The first is cut off, for a value
+// near the largest must not become an infinity (which itself leaves no
+// remainder); 16 bits remain, whose half is rounded off and leaves 8.
 __device__ __forceinline__ void split3(float x, float y, uint32_t (&o)[3]) {
   const uint32_t a = __float_as_uint(x) & 0xffff0000u, b = __float_as_uint(y) & 0xffff0000u;
   o[0] = (a >> 16) | b;

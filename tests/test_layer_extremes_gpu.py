@@ -5,7 +5,7 @@ import torch
 
 import muon_step_03_amd as M
 
-from _layers import (ROW, U, check_backward, check_weight, f64, grads, hidden, params,
+from _layers import (DEV, HALF, ROW, U, check_backward, check_weight, f64, grads, hidden, params,
                      within)
 
 pytestmark = pytest.mark.gpu
@@ -31,6 +31,27 @@ def test_weight_grad_of_the_largest_activations(tokens, rows, cols, dtype, fmt, 
         G = M.weight_grad(dy, ck, dtype=gdtype)
         assert not G[0].any()
         check_weight(G, dy, x64)
+
+
+@pytest.mark.parametrize("exponent", [-100, -108, -112, -120, -128, -136, -146])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens,rows,cols", SIZES)
+def test_weight_grad_of_tiny_gradients(tokens, rows, cols, dtype, exponent):
+    """dy down to subnormal numbers against activations so large that G is not.
+    float32 dy may lose half of bf16's smallest step, 2^-134, per element."""
+    g = torch.Generator().manual_seed(-exponent)
+    x = (torch.randint(-127, 128, (tokens, cols), generator=g) * 2.0 ** 90).to(dtype).to(DEV)
+    dy = torch.randn(tokens, rows, generator=g, dtype=torch.float64) * 2.0 ** exponent
+    dy = dy.to(dtype).to(DEV)
+    x64, d64 = f64(x), f64(dy)
+    ck = M.checkpoint_save(x, "int8")
+    assert np.array_equal(f64(M.checkpoint_restore(ck, F32)), x64)
+    want = d64.T @ x64
+    parts, lost = (1, 0.0) if dtype == BF16 else (3, 2.0 ** -134)
+    bound = (parts * tokens + 4) * U * (np.abs(d64).T @ np.abs(x64)) + lost * np.abs(x64).sum(0)
+    for gdtype in (BF16, F32):
+        within(M.weight_grad(dy, ck, dtype=gdtype), want,
+               bound + HALF[gdtype] * (np.abs(want) + bound), "G")
 
 
 @pytest.mark.parametrize("cols", [7, 200, 777, 2304, 8200])
