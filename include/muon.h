@@ -371,6 +371,12 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
 #define MUON_WEIGHT_GRAD_MAX_COUNT (1 << 20)
 size_t muon_weight_grad_workspace_bytes(int64_t count, int with_offsets, int64_t tokens,
                                         int64_t rows, int64_t cols, int dtype);
+/* Side of the square tiles of G that a call of these sizes is computed in, 128
+ * or 256, where every row of dy starts on 16 bytes (others may take 128 instead);
+ * 0 for sizes that are refused.  Which one is the choice of an estimate of the
+ * time; profiles name the kernels of the two differently. */
+int muon_weight_grad_tile(int64_t count, int with_offsets, int64_t tokens, int64_t rows,
+                          int64_t cols, int dtype);
 int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x,
                      const int64_t* offsets, int64_t count, int64_t rows, void* G, int g_dtype,
                      int accumulate, void* workspace, size_t workspace_bytes, void* stream);

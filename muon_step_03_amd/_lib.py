@@ -45,7 +45,7 @@ EXPORTS = (
     "muon_adamw_step", "muon_adamw_step_grouped", "muon_step_grouped_noalloc",
     "muon_checkpoint_save", "muon_checkpoint_restore", "muon_layernorm_forward",
     "muon_layernorm_workspace_bytes", "muon_layernorm_backward",
-    "muon_weight_grad_workspace_bytes", "muon_weight_grad",
+    "muon_weight_grad_workspace_bytes", "muon_weight_grad_tile", "muon_weight_grad",
 )
 MUON_NUM_PHASES = 10
 
@@ -162,6 +162,8 @@ def lib():
     L.muon_layernorm_backward.restype = i32
     L.muon_weight_grad_workspace_bytes.argtypes = [i64, i32, i64, i64, i64, i32]
     L.muon_weight_grad_workspace_bytes.restype = ctypes.c_size_t
+    L.muon_weight_grad_tile.argtypes = [i64, i32, i64, i64, i64, i32]
+    L.muon_weight_grad_tile.restype = i32
     L.muon_weight_grad.argtypes = [p, i64, i32, ck, p, i64, i64, p, i32, i32, p,
                                    ctypes.c_size_t, p]
     L.muon_weight_grad.restype = i32

@@ -103,6 +103,11 @@ size_t weight_grad_bytes(const WeightGradPlan& plan) {
   return plan.pieces > 0 && n > 0 ? n + kAlign : 0;
 }
 
+bool weight_grad_sizes_ok(int64_t count, int64_t tokens, int64_t rows, int64_t cols, int dtype) {
+  return dtype_ok(dtype) && count >= 1 && count <= MUON_WEIGHT_GRAD_MAX_COUNT &&
+         sizes_ok(tokens, cols) && rows >= 1 && rows <= MUON_MAX_DIM;
+}
+
 char* align_ptr(void* p) {
   return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p) + kAlign - 1) / kAlign * kAlign);
 }
@@ -264,10 +269,17 @@ int muon_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t
 
 size_t muon_weight_grad_workspace_bytes(int64_t count, int with_offsets, int64_t tokens,
                                         int64_t rows, int64_t cols, int dtype) {
-  if (!dtype_ok(dtype) || count < 1 || count > MUON_WEIGHT_GRAD_MAX_COUNT || !sizes_ok(tokens, cols) || rows < 1 || rows > MUON_MAX_DIM)
-    return 0;
+  if (!weight_grad_sizes_ok(count, tokens, rows, cols, dtype)) return 0;
   return weight_grad_bytes(
       weight_grad_plan(count, tokens, rows, cols, with_offsets != 0, dtype == MUON_DTYPE_BF16));
+}
+
+int muon_weight_grad_tile(int64_t count, int with_offsets, int64_t tokens, int64_t rows,
+                          int64_t cols, int dtype) {
+  if (!weight_grad_sizes_ok(count, tokens, rows, cols, dtype)) return 0;
+  const WeightGradPlan plan =
+      weight_grad_plan(count, tokens, rows, cols, with_offsets != 0, dtype == MUON_DTYPE_BF16);
+  return plan.pieces <= 0 ? 0 : plan.wide ? 256 : 128;
 }
 
 int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x,
