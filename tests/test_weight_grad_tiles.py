@@ -223,3 +223,17 @@ def test_two_streams_and_a_replayed_graph():
 
 def copy_of(ck):
     return M.ActCheckpoint(ck.q.clone(), ck.scale.clone(), ck.cols)
+
+
+@pytest.mark.skipif(not os.path.exists(_lib.LIB_PATH), reason="libmuon.so not built")
+@pytest.mark.parametrize("tokens,rows,cols", [(65536, 1001, 8), (65536, 1000, 8), (16384, 4096, 1024),
+                                              (16384, 4095, 1024), (2049, 1001, 777), (96, 768, 768)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_workspace_holds_partial_sums_and_repacked_rows(tokens, rows, cols, dtype):
+    """At most 64 parts of one matrix, each G in float32; dy once more, in padded
+    rows of bf16, only where the large tiles take odd ones.  (float32 dy is split
+    on its way to LDS and needs no room.)"""
+    got = M.weight_grad_workspace_bytes(1, False, tokens, rows, cols, dtype)
+    repacked = dtype == BF16 and rows % 8 != 0 and tile(1, tokens, rows, cols, dtype, False) == 256
+    room = tokens * (rows + 7) // 8 * 8 * 2 if repacked else 0
+    assert room * 0.99 <= got <= 64 * rows * cols * 4 + room + 1024
