@@ -436,16 +436,27 @@ hipError_t backward(const LnBackward& p, hipStream_t s) {
 
 // The blocks that the CUs hold at once (a third one would only wait: float32
 // rows of 1024, 4099 of them, 14.9 us with 512 blocks, one per CU at a time, 11.6
-// with 256).  Up to kOneBlock passes of a block are left to a single one, which
-// spares the second launch: 12 rows of 768 in 5.4 us against 7.4; 64 in 8 passes
-// take 11.3 us against 6.7, but 3 us less of the host's time, which is longer.
-constexpr int64_t kOneBlock = 8;
+// with 256).  A few passes of a block are left to a single one, which spares the
+// second launch.  Measured in bf16, eager calls in a row and one of a captured
+// graph, one block against two launches:
+//   12 rows of 768, 2 passes     13.5 and 4.8 us against 17.8 and 6.2
+//   64 rows of 768, 8 passes     13.4 and 11.0   against 17.9 and 6.5
+//   16 rows of 4096, 8 passes    14.8 and 14.8   against 17.5 and 8.1
+//   3 rows of 8192               13.0 and 12.2   against 17.3 and 12.6
+//   2 rows of 16384              22.1 and 22.0   against 23.8 and 23.2
+//   3 rows of 16384              25.0 and 24.9   against 23.7 and 23.3
+//   2 rows of 32768              56.9 and 56.8   against 52.2 and 51.8
+// Up to 4096 columns 8 passes hide behind the host's time for a call; a captured
+// graph, where more than 3 lose, would sum in another order than the eager call if
+// it took two launches.  Above, where a pass is one row, one block is taken while it
+// is ahead in both.
+int64_t one_block_passes(int64_t cols) { return cols <= 4096 ? 8 : 1 + 16384 / cols; }
 int ln_backward_blocks(int64_t tokens, int64_t cols, bool bf16) {
   const RowShape r = row_shape(cols, true);
   const int nt = r.lpr < 1024 ? 512 : 1024, rows = nt / r.lpr;
   const int64_t want = (tokens + rows - 1) / rows;
   const int64_t cap = bwd_two_blocks(bf16, r.lpr, r.v) ? 512 : 256;
-  return int(want < 1 ? 0 : want <= kOneBlock ? 1 : want < cap ? want : cap);
+  return int(want < 1 ? 0 : want <= one_block_passes(cols) ? 1 : want < cap ? want : cap);
 }
 
 #define MUON_LN_SHAPE(CALL, LPR, V) \

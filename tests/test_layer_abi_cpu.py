@@ -223,3 +223,12 @@ def test_binding_refuses_what_is_not_on_a_gpu():
         M.ActCheckpoint(x, torch.zeros(4, 4, dtype=torch.uint8), 64)
     with pytest.raises(ValueError, match="format"):
         M.ActCheckpoint.empty(4, 64, "e5m2", device="cpu")
+
+
+def test_few_long_rows_are_not_left_to_one_block(L):
+    """One block of the norm's backward pass needs no workspace.  Rows of more
+    than 4096 columns are one pass each: a few of 8192, one of 32768."""
+    one = {4096: 16, 5632: 3, 8192: 3, 8193: 2, 16384: 2, 16385: 1, 32768: 1}
+    for cols, rows in one.items():
+        assert L.muon_layernorm_workspace_bytes(rows, cols) == 0, cols
+        assert L.muon_layernorm_workspace_bytes(rows + 1, cols) > 0, cols

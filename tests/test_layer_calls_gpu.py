@@ -180,3 +180,21 @@ def test_one_tensor_for_several_inputs():
     check_backward(M.layernorm_backward(x, x, v, out.mean, out.rstd), x, f64(x), v, out.mean, out.rstd)
     ck = M.checkpoint_save(x)
     check_weight(M.weight_grad(x, ck), x, f64(M.checkpoint_restore(ck, F32)))
+
+
+@pytest.mark.parametrize("cols,limit", [(4096, 16), (8192, 3), (16384, 2), (32768, 1)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_on_both_sides_of_one_block(cols, limit, dtype):
+    """The last number of rows that a single block takes, and one more."""
+    gain, bias = params(cols, dtype)
+    for tokens in (limit, limit + 1, limit + 5):
+        assert (M.layernorm_workspace_bytes(tokens, cols) == 0) == (tokens == limit)
+        x, dy = hidden(tokens, cols, dtype, 1), grads(tokens, cols, dtype, 1)
+        out = M.layernorm_forward(x, gain, bias)
+        check_backward(M.layernorm_backward(dy, x, gain, out.mean, out.rstd), dy, f64(x), gain,
+                       out.mean, out.rstd)
+        dgain, dbias = params(cols, dtype, seed=9)
+        before = (dgain.clone(), dbias.clone())
+        got = M.layernorm_backward(dy, x, gain, out.mean, out.rstd, dgain=dgain, dbias=dbias,
+                                   accumulate=True)
+        check_backward(got, dy, f64(x), gain, out.mean, out.rstd, before)
