@@ -12,8 +12,9 @@
 //
 // Bound by the matrix cores for many tokens (an element of G takes 2 flops per
 // token, of dy and x 2 cols and 2 rows).  Measured on one MI355X, 4096 x 1024 over
-// 16384 tokens: bf16 dy 126 to 135 us with e4m3 x (1060 TFLOP/s; 98.6 us at the
-// rate of a large library product), 129 to 137 with int8; float32 dy 424 us.  For
+// 16384 tokens: bf16 dy 123 us with e4m3 x in a row of the same call, 131 among
+// others (1050 TFLOP/s; 98.6 us at the rate of a large library product), 127 with
+// int8; float32 dy 424 to 441 us.  For
 // few tokens it is bound by the latency of a launch and one tile (768 x 768 over
 // 96: 5.4 us), in between by the partial sums' traffic.
 //
@@ -53,15 +54,19 @@ static_assert(sizeof(Split) == kWeightGradSplitBytes, "size of the table");
 // offsets are clamped to [0, tokens] and read as the largest so far, so that
 // no piece leaves the buffers and their number is bounded whatever the offsets
 // hold.  A matrix's tokens are shared evenly between its pieces, in whole
-// steps.  Up to 1024 matrices, pieces are put in order of their length,
+// steps.  Up to 128 matrices, pieces are put in order of their length,
 // longest first: blocks start in this order, so that all end together.  Up to
-// 64 matrices need one wave (NT = 64).
-constexpr int kPlanThreads = 1024;
+// 64 matrices need one wave (NT = 64), up to 128 are compared by all threads, a
+// share of them each.  Ordered against as they come, uneven, bf16, int8 x: 96 of
+// 1408 x 512 over 49152 tokens 108 and 136 us, 128 of 768 x 512 70.5 and 79, 128 of
+// 128 x 128 over 16384 20.0 and 18.7; ordering 256 of 1408 x 512 gains nothing (176)
+// and of 128 x 128 costs 6 of 18.  The plan takes 6 to 7 us ordered, 5 unordered.
+constexpr int kPlanThreads = 1024, kPlanOrdered = 128;
 template <int NT>
 __global__ __launch_bounds__(NT) void plan_kernel(const WeightGrad p) {
-  constexpr int WAVES = NT / 64;
+  constexpr int WAVES = NT / 64, SHARES = NT / kPlanOrdered;
   __shared__ int wave_top[WAVES], wave_n[WAVES], wave_m[WAVES], wave_s[WAVES];
-  __shared__ int keys[NT], counts[NT];
+  __shared__ int keys[NT], counts[NT], ranks[NT];
   Piece* table = static_cast<Piece*>(p.table);
   Split* splits = reinterpret_cast<Split*>(table + p.pieces);
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -116,18 +121,23 @@ __global__ __launch_bounds__(NT) void plan_kernel(const WeightGrad p) {
       slot += wave_m[w];
       at += wave_s[w];
     }
-    if (p.count <= NT) {
+    if constexpr (NT == 64) {
       first = 0;
-      if constexpr (NT == 64) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) {   // lanes past the last matrix have no pieces
-          const int kj = __builtin_amdgcn_readlane(share, j), nj = __builtin_amdgcn_readlane(n, j);
-          first += kj > share || (kj == share && j < t) ? nj : 0;
-        }
-      } else {
-        for (int j = 0; j < p.count; ++j)
-          first += keys[j] > share || (keys[j] == share && j < t) ? counts[j] : 0;
+      for (int j = 0; j < 64; ++j) {   // lanes past the last matrix have no pieces
+        const int kj = __builtin_amdgcn_readlane(share, j), nj = __builtin_amdgcn_readlane(n, j);
+        first += kj > share || (kj == share && j < t) ? nj : 0;
       }
+    } else if (p.count <= kPlanOrdered) {
+      const int me = t % kPlanOrdered, key = keys[me];
+      int s = 0;
+      for (int j = t / kPlanOrdered; j < p.count; j += SHARES)
+        s += keys[j] > key || (keys[j] == key && j < me) ? counts[j] : 0;
+      ranks[t] = s;
+      __syncthreads();
+      first = 0;
+#pragma unroll
+      for (int i = 0; i < SHARES; ++i) first += ranks[i * kPlanOrdered + me];
     }
     for (int j = 0; j < n; ++j) {
       Piece pc{};

@@ -198,3 +198,22 @@ def test_rows_on_both_sides_of_one_block(cols, limit, dtype):
         got = M.layernorm_backward(dy, x, gain, out.mean, out.rstd, dgain=dgain, dbias=dbias,
                                    accumulate=True)
         check_backward(got, dy, f64(x), gain, out.mean, out.rstd, before)
+
+
+@pytest.mark.parametrize("count", [63, 64, 65, 100, 127, 128, 129, 1023, 1024, 1025])
+@pytest.mark.parametrize("rows,cols", [(40, 72), (512, 512)])
+def test_numbers_of_matrices_at_the_plans_borders(count, rows, cols):
+    """One wave, one block that orders the pieces, one that does not, several
+    rounds of it: uneven matrices, many of one length, cut and whole, exact."""
+    g = torch.Generator().manual_seed(count)
+    counts = torch.randint(0, 40, (count,), generator=g)
+    counts[torch.rand(count, generator=g) < 0.2] = 0
+    counts[torch.rand(count, generator=g) < 0.2] = 32
+    counts[count // 2], counts[-1] = 1500, 700
+    off = [0] + counts.cumsum(0).tolist()
+    dy = torch.randint(-9, 10, (off[-1] + 3, rows), generator=g).to(BF16).to(DEV)
+    x = torch.randint(-9, 10, (off[-1] + 3, cols), generator=g).to(BF16).to(DEV)
+    G = M.weight_grad(dy, M.checkpoint_save(x, "int8"), dtype=F32,
+                      offsets=torch.tensor(off, dtype=torch.int64, device=DEV))
+    for e, (a, b) in enumerate(zip(off[:-1], off[1:])):
+        assert torch.equal(G[e].double(), dy[a:b].t().double() @ x[a:b].double()), e
