@@ -278,15 +278,16 @@ int muon_adamw_step_grouped(const muon_adamw_tensor* tensors, int64_t count, int
  * ([-117, 121]), and rounds x * 2^-e to the nearest q, ties to even; what the
  * largest exponent cannot hold saturates.  A block with an infinity or a NaN
  * gets scale 255 and reads as NaN throughout; a zero block gets exponent -117.
- * Padding bytes are written as zero.  With a power of two as scale and at most
+ * Padding bytes are written as zero.  Reading is defined for what a save
+ * writes: scales in that range (10 to 246, or 248) or 255.  With a power of two as scale and at most
  * 8 significant bits in q, every value read back is exact in bfloat16 and
  * float32, so the weight gradient's products on bf16 matrix cores have no
  * second rounding of the activation.
  *
  *  Memory   x, y, dy, dx: DEVICE pointers to tokens x cols matrices of `dtype`
  *           with unit column stride.  Inputs x and dy have a row stride (ldx,
- *           lddy, in elements, at least the row length), outputs y and dx are
- *           contiguous.  gain, bias, dgain, dbias: cols elements of
+ *           lddy, in elements, at least the row length and at most 2^24),
+ *           outputs y and dx are contiguous.  gain, bias, dgain, dbias: cols elements of
  *           `param_dtype`.  mean, rstd: float32, one per token.  q must be
  *           16-byte and scale 4-byte aligned; every other pointer needs its
  *           element's alignment only (aligned rows are faster for dy of the
@@ -329,7 +330,8 @@ int muon_checkpoint_restore(const muon_ckpt* ckpt, void* x, int dtype, void* str
  * row in registers:
  *   mean = sum_c x / cols,  rstd = 1 / sqrt(sum_c (x - mean)^2 / cols + eps)
  *   y = (x - mean) * rstd * gain + bias        (bias may be NULL: none)
- * eps must be finite and >= 0.  x_ckpt and y_ckpt (each may be NULL) also save
+ * eps must be finite and >= 0.  A sum that leaves float32 is infinite: a row whose
+ * squares do (magnitudes above about 1e19) gets rstd = 0 and y = bias.  x_ckpt and y_ckpt (each may be NULL) also save
  * x, or y as rounded to `dtype`, in the same pass.
  */
 int muon_layernorm_forward(const void* x, int64_t ldx, const void* gain, const void* bias,

@@ -5,7 +5,8 @@ They make what the optimizer steps consume: ``layernorm_backward`` the
 gradients of gains and biases (the AdamW vectors), ``weight_grad`` the G of
 ``muon_step`` (one matrix) or of ``stacked_group`` (a stack of experts).  As in
 ``api``, every arithmetic step runs in the library's HIP kernels; PyTorch
-provides device memory and streams.
+provides device memory and streams.  The functions are not differentiable
+themselves: ``layers`` is.
 
 Matrices are tokens x columns, float32 or bfloat16, on one GPU.  Inputs may be
 row-strided views (a slice of a fused projection's columns); a column stride
