@@ -121,23 +121,24 @@ __global__ __launch_bounds__(NT) void plan_kernel(const WeightGrad p) {
       slot += wave_m[w];
       at += wave_s[w];
     }
-    if constexpr (NT == 64) {
+    if (p.count <= (NT == 64 ? 64 : kPlanOrdered)) {
       first = 0;
+      if constexpr (NT == 64) {
 #pragma unroll
-      for (int j = 0; j < 64; ++j) {   // lanes past the last matrix have no pieces
-        const int kj = __builtin_amdgcn_readlane(share, j), nj = __builtin_amdgcn_readlane(n, j);
-        first += kj > share || (kj == share && j < t) ? nj : 0;
+        for (int j = 0; j < 64; ++j) {   // lanes past the last matrix have no pieces
+          const int kj = __builtin_amdgcn_readlane(share, j), nj = __builtin_amdgcn_readlane(n, j);
+          first += kj > share || (kj == share && j < t) ? nj : 0;
+        }
+      } else {
+        const int me = t % kPlanOrdered, key = keys[me];
+        int s = 0;
+        for (int j = t / kPlanOrdered; j < p.count; j += SHARES)
+          s += keys[j] > key || (keys[j] == key && j < me) ? counts[j] : 0;
+        ranks[t] = s;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < SHARES; ++i) first += ranks[i * kPlanOrdered + me];
       }
-    } else if (p.count <= kPlanOrdered) {
-      const int me = t % kPlanOrdered, key = keys[me];
-      int s = 0;
-      for (int j = t / kPlanOrdered; j < p.count; j += SHARES)
-        s += keys[j] > key || (keys[j] == key && j < me) ? counts[j] : 0;
-      ranks[t] = s;
-      __syncthreads();
-      first = 0;
-#pragma unroll
-      for (int i = 0; i < SHARES; ++i) first += ranks[i * kPlanOrdered + me];
     }
     for (int j = 0; j < n; ++j) {
       Piece pc{};

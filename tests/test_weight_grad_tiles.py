@@ -105,6 +105,24 @@ def test_every_number_of_steps_at_once(rows, cols, fmt, gdtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("start,more", [(8, 16), (3, 16), (8, 17)])
+def test_rows_that_the_large_tiles_cannot_read(start, more):
+    """A ragged call whose sizes take the large tiles, dy a view whose rows start
+    on 16 bytes, start elsewhere, or are an odd stride apart: the same bits."""
+    rows, cols = COUNTS_SIZES[0]
+    tokens = sum(COUNTS) + 7
+    assert tile(len(COUNTS), tokens, rows, cols) == 256
+    dy, x = integers(tokens, rows, cols, 5)
+    ck = M.checkpoint_save(x, "int8")
+    at = torch.tensor([0] + np.cumsum(COUNTS).tolist(), dtype=torch.int64, device=DEV)
+    wide = torch.full((tokens, rows + more), float("nan"), dtype=BF16, device=DEV)
+    view = wide[:, start:start + rows]
+    view.copy_(dy)
+    want = M.weight_grad(dy, ck, offsets=at, dtype=F32)
+    assert torch.equal(M.weight_grad(view, ck, offsets=at, dtype=F32), want)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,cols", APART)
 def test_bad_tokens_stay_apart(rows, cols):
     """Marked blocks, NaN and infinities of one matrix's tokens, and of its
