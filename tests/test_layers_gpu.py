@@ -233,3 +233,47 @@ def test_linear_of_inputs_that_do_not_fold(dtype, layout):
         to += [z.detach(), *torch.autograd.grad(z, X, b)]
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     check_weight(got[2], dz.reshape(42, 72), lo.checkpoint(f64(x.reshape(42, 136)), "e4m3")[0])
+
+
+@pytest.mark.parametrize("shape", [(0, 5, 64), (64,), (1, 64), (3, 1, 2, 64)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_layers_of_any_leading_dimensions(shape, dtype):
+    """No token, one without a leading dimension, several dimensions."""
+    x = hidden(max(1, int(np.prod(shape[:-1]))), 64, dtype, seed=1)[:int(np.prod(shape[:-1]))].view(shape)
+    X, gain, bias = leaf(x), *(leaf(p) for p in params(64, dtype))
+    W = leaf(hidden(24, 64, dtype, seed=3, scale=0.05))
+    y, ck = M.layer_norm(X, gain, bias, keep="int8", y_keep="e4m3")
+    z = M.linear(y, W, ck)
+    assert y.shape == shape and z.shape == (*shape[:-1], 24) and ck.tokens == x.numel() // 64
+    z.sum().backward()
+    for t in (X, gain, bias, W):
+        assert t.grad.shape == t.shape and bool(t.grad.isfinite().all())
+    if x.numel():
+        check_weight(W.grad, torch.ones(ck.tokens, 24, dtype=dtype, device=DEV),
+                     lo.checkpoint(f64(y.view(-1, 64)), "e4m3")[0])
+    else:
+        assert not W.grad.any() and not gain.grad.any() and not bias.grad.any()
+
+
+def test_shared_weights_broadcast_inputs_and_a_kept_graph():
+    """A weight and a norm used twice, an input repeated along a batch, a graph
+    run backward twice: gradients add up as PyTorch's do."""
+    x = hidden(7, 64, F32, seed=1)
+    X, gain, W = leaf(x), leaf(params(64, F32)[0]), leaf(hidden(64, 64, F32, seed=3, scale=0.05))
+    wide = X.expand(5, 7, 64)
+    z = M.linear(M.layer_norm(M.linear(M.layer_norm(wide, gain), W, "int8"), gain), W, "int8")
+    dz = grads(35, 64, F32, seed=2).view(5, 7, 64)
+    first = torch.autograd.grad(z, (X, gain, W), dz, retain_graph=True)
+    again = torch.autograd.grad(z, (X, gain, W), dz)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    # the same from separate leaves, added
+    parts = [leaf(t.detach()) for t in (x.expand(5, 7, 64).contiguous(), gain, W, gain, W)]
+    A, g1, W1, g2, W2 = parts
+    z = M.linear(M.layer_norm(M.linear(M.layer_norm(A, g1), W1, "int8"), g2), W2, "int8")
+    dA, dg1, dW1, dg2, dW2 = torch.autograd.grad(z, parts, dz)
+    u = 2.0 ** -24
+    for got, want, terms in ((first[0], dA.double().sum(0), dA.double().abs().sum(0)),
+                             (first[1], dg1.double() + dg2.double(), dg1.abs().double() + dg2.abs().double()),
+                             (first[2], dW1.double() + dW2.double(), dW1.abs().double() + dW2.abs().double())):
+        # at most five additions in float32
+        assert bool(((got.double() - want).abs() <= 5 * u * terms).all())
