@@ -261,6 +261,81 @@ int muon_adamw_step_grouped(const muon_adamw_tensor* tensors, int64_t count, int
                             double beta1, double beta2, double eps, int64_t step, void* stream);
 
 /*
+ * The same step with both moments kept in 8 bits: 2.06 bytes of state per
+ * element instead of 8.  The state holds m and the root r = sqrt(v), each a
+ * byte per element with one power-of-two scale per MUON_CKPT_BLOCK = 32
+ * elements in a row (of the flattened tensor); per element, in float32:
+ *
+ *   m' = beta1 m + (1 - beta1) g
+ *   r' = sqrt(beta2 r^2 + (1 - beta2) g^2)
+ *   p' = (1 - lr wd) p - lr (m' / (1 - beta1^t)) / (r' / sqrt(1 - beta2^t) + eps)
+ *
+ * p' is made from m' and r' before they are rounded to 8 bits.
+ *
+ * State format.  An element stands for q * 2^(scale - 127).  q of m is an OCP
+ * e4m3 number; q of r is a number without a sign, 4 bits of exponent (bias 7)
+ * and 4 of mantissa, no infinities: byte c stands for (1 + c % 16 / 16) *
+ * 2^(c / 16 - 7), or c * 2^-10 where c < 16; 496 is the largest.  (The root
+ * has half of v's range in exponents, which a byte can hold.)  A block's
+ * scale is the smallest that brings its largest magnitude into the format's
+ * range, exponents -117 to 119 (r: -116 to 118).  Elements are rounded
+ * stochastically: a magnitude a = (k + f) step, k whole, goes to k + 1 where
+ * f + (u + 1/2) / 65536 >= 1 and to k otherwise, never past the largest
+ * number; u is the upper (r: the lower) half of 32 bits made of the tensor's
+ * seed and the element's index i:
+ *
+ *   x = (i mod 2^32) 0x9e3779b1 + (i / 2^32) 0x85ebca77 + seed   (mod 2^32)
+ *   x = (x ^ x >> 16) 0x7feb352d;  x = (x ^ x >> 15) 0x846ca68b;  x = x ^ x >> 16
+ *
+ * Rounding to nearest would hold a slowly moving average where it is: with
+ * beta2 = 0.999 no step of r reaches half a step of the format.  The caller
+ * gives every tensor and step another seed; the same seed gives the same
+ * bits.  An r that is not zero is never kept as zero, so that m / r stays
+ * bounded.  A block with an infinity or a NaN gets scale 255 and reads as NaN
+ * throughout (r' is infinite for a gradient of 2^64 or more, whose square
+ * leaves float32).  A state of zero bytes stands for zeros.
+ *
+ *  Memory   P, G as for muon_adamw_step.  m_q, r_q: DEVICE arrays of n bytes
+ *           up to a multiple of 32 (bytes behind the n-th are written as
+ *           zero), 16-byte aligned; m_scale, r_scale: one byte per block.  No
+ *           buffer may overlap another, within a tensor or across the tensors
+ *           of one call.
+ *  Sizes    0 <= n <= MUON_ADAMW8_MAX_ELEMENTS; n == 0 skips the tensor.
+ *  Scalars, stream, errors  as for muon_adamw_step_grouped; one launch per
+ *           MUON_ADAMW8_TENSORS_PER_LAUNCH tensors.
+ */
+#define MUON_ADAMW8_MAX_ELEMENTS (((int64_t)1) << 35)
+#define MUON_ADAMW8_TENSORS_PER_LAUNCH 48
+
+typedef struct muon_adamw8_state {
+  void* m_q;        /* e4m3, n bytes up to a multiple of 32 */
+  uint8_t* m_scale; /* one per 32 elements */
+  uint8_t* r_q;
+  uint8_t* r_scale;
+  int64_t n;        /* elements */
+} muon_adamw8_state;
+
+typedef struct muon_adamw8_tensor {
+  void* P;             /* parameters, `dtype` */
+  const void* G;       /* gradients, `dtype` */
+  muon_adamw8_state state;
+  double lr;
+  double weight_decay;
+  uint32_t seed;       /* of the rounding */
+} muon_adamw8_tensor;
+
+/* One AdamW step with 8-bit states on `count` tensors.  `tensors` is a HOST
+ * array. */
+int muon_adamw_byte_step_grouped(const muon_adamw8_tensor* tensors, int64_t count, int dtype,
+                             double beta1, double beta2, double eps, int64_t step, void* stream);
+
+/* The values that `count` states stand for (r, not v), one state behind the
+ * other: m and r are DEVICE arrays of `dtype` with as many elements as the
+ * states together; exact in float32 and bfloat16.  `states` is a HOST array. */
+int muon_adamw_byte_moments(const muon_adamw8_state* states, int64_t count, void* m, void* r,
+                        int dtype, void* stream);
+
+/*
  * Layer operators: what a training step computes around the hidden weights
  * and hands to the steps above.  Layer norm gives y forward and dx, dgain and
  * dbias backward (gain and bias are the hybrid optimizer's AdamW vectors);

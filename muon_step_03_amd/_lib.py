@@ -31,6 +31,8 @@ MUON_MAX_NS_STEPS = 100
 MUON_GROUPS_PER_LAUNCH = 8
 MUON_ADAMW_MAX_ELEMENTS = 1 << 40
 MUON_ADAMW_TENSORS_PER_LAUNCH = 32
+MUON_ADAMW8_MAX_ELEMENTS = 1 << 35
+MUON_ADAMW8_TENSORS_PER_LAUNCH = 48
 MUON_NOALLOC_WORKSPACE_BYTES = 64 << 20
 MUON_MAX_TOKENS = 1 << 30
 MUON_CKPT_BLOCK = 32
@@ -46,6 +48,7 @@ EXPORTS = (
     "muon_checkpoint_save", "muon_checkpoint_restore", "muon_layernorm_forward",
     "muon_layernorm_workspace_bytes", "muon_layernorm_backward",
     "muon_weight_grad_workspace_bytes", "muon_weight_grad_tile", "muon_weight_grad",
+    "muon_adamw_byte_step_grouped", "muon_adamw_byte_moments",
 )
 MUON_NUM_PHASES = 10
 
@@ -73,6 +76,27 @@ class AdamwTensor(ctypes.Structure):
         ("n", ctypes.c_int64),
         ("lr", ctypes.c_double),
         ("weight_decay", ctypes.c_double),
+    ]
+
+
+class Adamw8State(ctypes.Structure):
+    _fields_ = [
+        ("m_q", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("r_q", ctypes.c_void_p),
+        ("r_scale", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+    ]
+
+
+class Adamw8Tensor(ctypes.Structure):
+    _fields_ = [
+        ("P", ctypes.c_void_p),
+        ("G", ctypes.c_void_p),
+        ("state", Adamw8State),
+        ("lr", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("seed", ctypes.c_uint32),
     ]
 
 
@@ -147,6 +171,11 @@ def lib():
                                           ctypes.c_int64, ctypes.c_void_p]
     L.muon_adamw_step_grouped.restype = ctypes.c_int
     p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    L.muon_adamw_byte_step_grouped.argtypes = [ctypes.POINTER(Adamw8Tensor), i64, i32, ctypes.c_double,
+                                           ctypes.c_double, ctypes.c_double, i64, p]
+    L.muon_adamw_byte_step_grouped.restype = i32
+    L.muon_adamw_byte_moments.argtypes = [ctypes.POINTER(Adamw8State), i64, p, p, i32, p]
+    L.muon_adamw_byte_moments.restype = i32
     ck = ctypes.POINTER(Ckpt)
     L.muon_checkpoint_save.argtypes = [p, i64, i32, ck, p]
     L.muon_checkpoint_save.restype = i32

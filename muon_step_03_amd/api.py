@@ -500,26 +500,166 @@ def adamw_step_grouped(tensors: Sequence[_lib.AdamwTensor], dtype: torch.dtype, 
     _check(st, "muon_adamw_step_grouped")
 
 
+class AdamwState8:
+    """Both moments of a tensor of ``n`` elements in 8 bits (``include/muon.h``,
+    "State format"): ``m_q`` (float8_e4m3fn) and ``r_q`` (uint8) hold n bytes up
+    to a multiple of 32, ``m_scale`` and ``r_scale`` (uint8) one byte per 32
+    elements.  m_q stands for the first moment, r_q for the root of the second."""
+
+    __slots__ = ("m_q", "m_scale", "r_q", "r_scale", "n", "device", "_c")
+
+    def __init__(self, m_q, m_scale, r_q, r_scale, n: int):
+        n = int(n)
+        blocks = (n + 31) // 32
+        if not 0 <= n <= _lib.MUON_ADAMW8_MAX_ELEMENTS:
+            raise ValueError(f"a state has at most {_lib.MUON_ADAMW8_MAX_ELEMENTS} elements, not {n}")
+        for name, t, numel, dtype in (("m_q", m_q, 32 * blocks, torch.float8_e4m3fn),
+                                      ("m_scale", m_scale, blocks, torch.uint8),
+                                      ("r_q", r_q, 32 * blocks, torch.uint8),
+                                      ("r_scale", r_scale, blocks, torch.uint8)):
+            _check_flat(name, t, numel, dtype)
+            if t.device != m_q.device:
+                raise ValueError(f"{name} is on {t.device}, m_q on {m_q.device}")
+        self.m_q, self.m_scale, self.r_q, self.r_scale, self.n = m_q, m_scale, r_q, r_scale, n
+        self.device = m_q.device
+        self._c = _lib.Adamw8State(m_q.data_ptr(), m_scale.data_ptr(), r_q.data_ptr(),
+                                   r_scale.data_ptr(), n)
+
+    @classmethod
+    def zeros(cls, n: int, device="cuda") -> "AdamwState8":
+        """The state before the first step."""
+        blocks = (int(n) + 31) // 32
+        size = 32 * blocks
+        buf = torch.zeros(2 * size + 2 * blocks, dtype=torch.uint8, device=device)
+        return cls(buf[:size].view(torch.float8_e4m3fn), buf[2 * size:2 * size + blocks],
+                   buf[size:2 * size], buf[2 * size + blocks:], n)
+
+    def __reduce__(self):      # copies and pickles have tensors of their own
+        return AdamwState8, (self.m_q, self.m_scale, self.r_q, self.r_scale, self.n)
+
+    @property
+    def nbytes(self) -> int:
+        return 2 * (self.m_q.numel() + self.m_scale.numel())
+
+    def __repr__(self):
+        return f"AdamwState8({self.n} elements, {self.device})"
+
+
+def adamw8_tensor(P, G, state: AdamwState8, *, lr, weight_decay=AUX_WEIGHT_DECAY,
+                  seed: int = 0) -> _lib.Adamw8Tensor:
+    """Descriptor of one tensor for :func:`adamw8_step_grouped` (the caller
+    keeps P, G and the state alive until the step has run).  ``seed`` (its low
+    32 bits) draws the roundings: every tensor and step takes another one; it
+    may be set anew in a descriptor that is kept."""
+    if not isinstance(state, AdamwState8):
+        raise TypeError("state must be an AdamwState8")
+    _check_flat("P", P, state.n)
+    dtype_code(P.dtype)
+    _check_flat("G", G, state.n, P.dtype)
+    for name, t in (("G", G), ("state", state)):
+        if t.device != P.device:
+            raise ValueError(f"{name} is on {t.device}, P on {P.device}")
+    return _lib.Adamw8Tensor(P.data_ptr(), G.data_ptr(), state._c, float(lr), float(weight_decay),
+                             int(seed) & 0xffffffff)
+
+
+def _c_array(kind, items):
+    """The items as a C array (one that is one already, as it is)."""
+    if isinstance(items, ctypes.Array) and items._type_ is kind:
+        return items, len(items)
+    items = list(items)
+    for x in items:
+        if type(x) is not kind:
+            raise TypeError(f"expected {kind.__name__} descriptors, got {type(x).__name__}")
+    # (in one copy: a constructor call with 49 of them takes 12 us, this 3)
+    return (kind * len(items)).from_buffer_copy(b"".join(items)), len(items)
+
+
+def adamw8_step_grouped(tensors: Sequence[_lib.Adamw8Tensor], dtype: torch.dtype, *, step,
+                        betas=AUX_BETAS, eps=AUX_EPS, stream=None):
+    """One AdamW step with 8-bit states on many tensors of one dtype, in place
+    on P and the states, one launch per ``MUON_ADAMW8_TENSORS_PER_LAUNCH``
+    tensors.  ``step`` counts updates from 1.  The current device must be that
+    of the tensors."""
+    arr, count = _c_array(_lib.Adamw8Tensor, tensors)
+    st = _lib.lib().muon_adamw_byte_step_grouped(arr, count, dtype_code(dtype), float(betas[0]),
+                                             float(betas[1]), float(eps), int(step),
+                                             _stream_handle(stream))
+    _check(st, "muon_adamw_byte_step_grouped")
+
+
+def adamw8_step(P, G, state: AdamwState8, *, lr, step, seed: int = 0, betas=AUX_BETAS, eps=AUX_EPS,
+                weight_decay=AUX_WEIGHT_DECAY, stream=None):
+    """One AdamW step with an 8-bit state on one tensor, in place on P and the
+    state."""
+    t = adamw8_tensor(P, G, state, lr=lr, weight_decay=weight_decay, seed=seed)
+    with torch.cuda.device(P.device):
+        adamw8_step_grouped([t], P.dtype, step=step, betas=betas, eps=eps, stream=stream)
+
+
+def adamw8_moments(states: Sequence[AdamwState8], dtype: torch.dtype = torch.float32, *, stream=None):
+    """``(m, r)``: the values that the states stand for, one state behind the
+    other, each a new vector of ``dtype`` (exact in float32 and bfloat16).  r
+    is the root of the second moment."""
+    states = [states] if isinstance(states, AdamwState8) else list(states)
+    if not states:
+        raise ValueError("no states")
+    total, device = 0, getattr(states[0], "device", None)
+    for i, s in enumerate(states):
+        if type(s) is not AdamwState8:
+            raise TypeError(f"states[{i}] must be an AdamwState8")
+        if s.device != device:
+            raise ValueError(f"states[{i}] is on {s.device}, expected {device}")
+        total += s.n
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the states on {device}")
+    arr, count = _c_array(_lib.Adamw8State, [s._c for s in states])
+    code = dtype_code(dtype)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        m = torch.empty(total, dtype=dtype, device=device)
+        r = torch.empty_like(m)
+        st = _lib.lib().muon_adamw_byte_moments(arr, count, m.data_ptr(), r.data_ptr(), code,
+                                            _stream_handle(None))
+    _check(st, "muon_adamw_byte_moments")
+    return m, r
+
+
 class AdamWStep:
     """AdamW over parameter groups (dicts with ``params``, ``lr`` and optional
-    ``weight_decay``), float32 moments per parameter, every parameter of one
-    dtype updated by one grouped call per step from its ``.grad``."""
+    ``weight_decay``), every parameter of one dtype updated by one grouped call
+    per step from its ``.grad``.
+
+    ``states``: "f32" keeps both moments in float32, "8bit" in an
+    :class:`AdamwState8` per parameter (``self.states``), whose roundings
+    follow from ``seed``, the step and the parameter's place."""
 
     def __init__(self, param_groups, betas=AUX_BETAS, eps=AUX_EPS,
-                 weight_decay=AUX_WEIGHT_DECAY):
+                 weight_decay=AUX_WEIGHT_DECAY, states="f32", seed: int = 0):
+        if states not in ("f32", "8bit"):
+            raise ValueError(f"unknown states {states!r}; expected 'f32' or '8bit'")
         self.betas = tuple(betas)
         self.eps = float(eps)
-        self.entries = []   # (param, m, v, lr, weight_decay)
+        self.seed = int(seed)
+        self.entries = []   # (param, m, v, lr, weight_decay); no m and v with 8-bit states
+        self.states = [] if states == "8bit" else None
         for gi, grp in enumerate(param_groups):
             lr = grp["lr"]
             wd = grp.get("weight_decay", weight_decay)
             for p in grp["params"]:
                 _check_flat(f"group {gi} param", p.data)
                 dtype_code(p.dtype)
-                self.entries.append((p, torch.zeros(p.numel(), dtype=torch.float32, device=p.device),
-                                     torch.zeros(p.numel(), dtype=torch.float32, device=p.device),
-                                     lr, wd))
+                m = v = None
+                if self.states is None:
+                    m = torch.zeros(p.numel(), dtype=torch.float32, device=p.device)
+                    v = torch.zeros(p.numel(), dtype=torch.float32, device=p.device)
+                else:
+                    self.states.append(AdamwState8.zeros(p.numel(), p.device))
+                self.entries.append((p, m, v, lr, wd))
         self.step_count = 0
+
+    def _seed(self, i):
+        """Of parameter i in the current step: any two differ."""
+        return (self.seed + 0x9e3779b1 * (self.step_count * len(self.entries) + i)) & 0xffffffff
 
     @torch.no_grad()
     def step(self):
@@ -529,9 +669,12 @@ class AdamWStep:
             if p.grad is None:
                 raise RuntimeError(f"AdamW parameter {i} has no gradient")
             by_dtype.setdefault(p.dtype, []).append(
-                adamw_tensor(p.data, p.grad, m, v, lr=lr, weight_decay=wd))
+                adamw_tensor(p.data, p.grad, m, v, lr=lr, weight_decay=wd) if self.states is None else
+                adamw8_tensor(p.data, p.grad, self.states[i], lr=lr, weight_decay=wd,
+                              seed=self._seed(i)))
+        call = adamw_step_grouped if self.states is None else adamw8_step_grouped
         for dtype, tensors in by_dtype.items():
-            adamw_step_grouped(tensors, dtype, step=self.step_count, betas=self.betas, eps=self.eps)
+            call(tensors, dtype, step=self.step_count, betas=self.betas, eps=self.eps)
 
 
 class HybridMuonAdamW:
