@@ -459,6 +459,64 @@ int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x
                      int accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Products of `count` (<= MUON_LINEAR_MAX_COUNT) linear layers y = x W^T, one
+ * matrix or one per expert, in the stacked layout of muon_group:
+ *   forward     y[t]  = x[t] W[e]^T     for the tokens t of matrix e
+ *   input grad  dx[t] = dy[t] W[e]
+ * x: tokens x cols, y and dy: tokens x rows, W: [count][rows][cols], all of
+ * `dtype`; x and dy have a row stride (in elements), y, dx and W are
+ * contiguous.  offsets: DEVICE array of count + 1 int64 as for
+ * muon_weight_grad, read on the device only; NULL with count == 1 takes every
+ * token.  Outputs of tokens that belong to no matrix are zero, and so are all
+ * with count == 0 (its one offset is read like any other).  Products are exact
+ * in float32 (bf16) or rounded to it (float32), accumulated in float32 and
+ * rounded once to `dtype`.  Sizes, strides, stream and errors as for the other
+ * layer operators; no workspace.
+ */
+#define MUON_LINEAR_MAX_COUNT 1024
+int muon_linear_forward(const void* x, int64_t ldx, int dtype, const void* W,
+                        const int64_t* offsets, int64_t count, int64_t tokens, int64_t rows,
+                        int64_t cols, void* y, void* stream);
+int muon_linear_input_grad(const void* dy, int64_t lddy, int dtype, const void* W,
+                           const int64_t* offsets, int64_t count, int64_t tokens, int64_t rows,
+                           int64_t cols, void* dx, void* stream);
+
+/*
+ * The same from 8-bit operands.  x (or dy) is a checkpoint in e4m3
+ * (MUON_CKPT_E4M3; a power-of-two scale per 32 columns).  W holds e4m3 numbers
+ * with a power-of-two scale per block of MUON_WEIGHT_BLOCK x MUON_WEIGHT_BLOCK
+ * = 128 x 128, chosen and rounded as a checkpoint's are (a block with an
+ * infinity or a NaN gets scale 255 and reads as NaN), twice: q with rows of
+ * MUON_WEIGHT_PITCH(cols) bytes and q_t, rows and columns exchanged, with rows
+ * of MUON_WEIGHT_PITCH(rows) bytes, padded with zeros.  An element stands for
+ * q * 2^(scale - 127); the product multiplies and adds these values in float32
+ * on the matrix cores, which take the scales with the operands, and rounds
+ * once to `dtype`.
+ *  Memory   q and q_t 16-byte aligned.  Reading is defined for what
+ *           muon_weight_quantize writes.
+ */
+#define MUON_WEIGHT_BLOCK 128
+#define MUON_WEIGHT_PITCH(n) (((n) + 127) / 128 * 128)
+
+typedef struct muon_weight8 {
+  void* q;         /* [count][rows][MUON_WEIGHT_PITCH(cols)] */
+  void* q_t;       /* [count][cols][MUON_WEIGHT_PITCH(rows)] */
+  uint8_t* scale;  /* [count][row blocks][column blocks] */
+  int64_t count;   /* 1 for a single matrix */
+  int64_t rows;
+  int64_t cols;
+} muon_weight8;
+
+/* Quantizes contiguous W [count][rows][cols] of `dtype`. */
+int muon_weight_quantize(const void* W, int dtype, const muon_weight8* out, void* stream);
+
+/* tokens and the inner size are those of the checkpoint; dtype: of y (dx). */
+int muon_linear_forward_quantized(const muon_ckpt* x, const muon_weight8* W,
+                                  const int64_t* offsets, void* y, int dtype, void* stream);
+int muon_linear_input_grad_quantized(const muon_ckpt* dy, const muon_weight8* W,
+                                     const int64_t* offsets, void* dx, int dtype, void* stream);
+
+/*
  * Phase timing, for benchmarks and profiling.  While enabled (process-wide),
  * every kernel launch of the step entry points is bracketed by two HIP events
  * recorded on the caller's stream.  muon_profile_read waits for the recorded

@@ -17,3 +17,4 @@ from .layer_ops import (  # noqa: F401
     layernorm_forward, layernorm_workspace_bytes, weight_grad, weight_grad_workspace_bytes,
 )
 from .layers import layer_norm, linear  # noqa: F401
+from .linear_ops import Weight8, linear_forward, linear_input_grad, weight_quantize  # noqa: F401

@@ -38,6 +38,8 @@ MUON_MAX_TOKENS = 1 << 30
 MUON_CKPT_BLOCK = 32
 MUON_CKPT_E4M3 = 0
 MUON_CKPT_INT8 = 1
+MUON_LINEAR_MAX_COUNT = 1024
+MUON_WEIGHT_BLOCK = 128
 
 # Every symbol include/muon.h declares.
 EXPORTS = (
@@ -49,6 +51,8 @@ EXPORTS = (
     "muon_layernorm_workspace_bytes", "muon_layernorm_backward",
     "muon_weight_grad_workspace_bytes", "muon_weight_grad_tile", "muon_weight_grad",
     "muon_adamw_byte_step_grouped", "muon_adamw_byte_moments",
+    "muon_linear_forward", "muon_linear_input_grad", "muon_weight_quantize",
+    "muon_linear_forward_quantized", "muon_linear_input_grad_quantized",
 )
 MUON_NUM_PHASES = 10
 
@@ -108,6 +112,22 @@ class Ckpt(ctypes.Structure):
         ("cols", ctypes.c_int64),
         ("format", ctypes.c_int),
     ]
+
+
+class Weight8(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("q_t", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("count", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+    ]
+
+
+def weight_pitch(n: int) -> int:
+    """Bytes per row of an 8-bit weight's q (MUON_WEIGHT_PITCH)."""
+    return (n + 127) // 128 * 128
 
 
 def ckpt_q_pitch(cols: int) -> int:
@@ -177,6 +197,15 @@ def lib():
     L.muon_adamw_byte_moments.argtypes = [ctypes.POINTER(Adamw8State), i64, p, p, i32, p]
     L.muon_adamw_byte_moments.restype = i32
     ck = ctypes.POINTER(Ckpt)
+    w8 = ctypes.POINTER(Weight8)
+    for fn in (L.muon_linear_forward, L.muon_linear_input_grad):
+        fn.argtypes = [p, i64, i32, p, p, i64, i64, i64, i64, p, p]
+        fn.restype = i32
+    for fn in (L.muon_linear_forward_quantized, L.muon_linear_input_grad_quantized):
+        fn.argtypes = [ck, w8, p, p, i32, p]
+        fn.restype = i32
+    L.muon_weight_quantize.argtypes = [p, i32, w8, p]
+    L.muon_weight_quantize.restype = i32
     L.muon_checkpoint_save.argtypes = [p, i64, i32, ck, p]
     L.muon_checkpoint_save.restype = i32
     L.muon_checkpoint_restore.argtypes = [ck, p, i32, p]
