@@ -481,6 +481,21 @@ int muon_linear_input_grad(const void* dy, int64_t lddy, int dtype, const void* 
                            const int64_t* offsets, int64_t count, int64_t tokens, int64_t rows,
                            int64_t cols, void* dx, void* stream);
 
+/* Which kernel computes a call of these sizes (quantized: from 8-bit operands,
+ * dtype that of the result) where every row starts on 16 bytes; others may take
+ * MUON_LINEAR_TILES_128 instead of the blocks that stay.  -1 for sizes that are
+ * refused.  The choice is one of measured and estimated times; profiles name the
+ * kernels differently. */
+enum {
+  MUON_LINEAR_FEW = 0,         /* 16 tokens x 16 outputs, k shared by four waves */
+  MUON_LINEAR_TILES_64 = 1,    /* tiles of 64 x 64, */
+  MUON_LINEAR_TILES_128 = 2,   /* of 128 x 128 */
+  MUON_LINEAR_STREAM_128 = 3,  /* blocks that stay, tiles of 128 x 128, */
+  MUON_LINEAR_STREAM_256 = 4   /* of 256 x 256 */
+};
+int muon_linear_kernel(int input_grad, int quantized, int64_t count, int64_t tokens, int64_t rows,
+                       int64_t cols, int dtype);
+
 /*
  * The same from 8-bit operands.  x (or dy) is a checkpoint in e4m3
  * (MUON_CKPT_E4M3; a power-of-two scale per 32 columns).  W holds e4m3 numbers

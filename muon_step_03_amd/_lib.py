@@ -39,6 +39,8 @@ MUON_CKPT_BLOCK = 32
 MUON_CKPT_E4M3 = 0
 MUON_CKPT_INT8 = 1
 MUON_LINEAR_MAX_COUNT = 1024
+MUON_LINEAR_FEW, MUON_LINEAR_TILES_64, MUON_LINEAR_TILES_128 = 0, 1, 2
+MUON_LINEAR_STREAM_128, MUON_LINEAR_STREAM_256 = 3, 4
 MUON_WEIGHT_BLOCK = 128
 
 # Every symbol include/muon.h declares.
@@ -52,7 +54,7 @@ EXPORTS = (
     "muon_weight_grad_workspace_bytes", "muon_weight_grad_tile", "muon_weight_grad",
     "muon_adamw_byte_step_grouped", "muon_adamw_byte_moments",
     "muon_linear_forward", "muon_linear_input_grad", "muon_weight_quantize",
-    "muon_linear_forward_quantized", "muon_linear_input_grad_quantized",
+    "muon_linear_forward_quantized", "muon_linear_input_grad_quantized", "muon_linear_kernel",
 )
 MUON_NUM_PHASES = 10
 
@@ -204,6 +206,8 @@ def lib():
     for fn in (L.muon_linear_forward_quantized, L.muon_linear_input_grad_quantized):
         fn.argtypes = [ck, w8, p, p, i32, p]
         fn.restype = i32
+    L.muon_linear_kernel.argtypes = [i32, i32, i64, i64, i64, i64, i32]
+    L.muon_linear_kernel.restype = i32
     L.muon_weight_quantize.argtypes = [p, i32, w8, p]
     L.muon_weight_quantize.restype = i32
     L.muon_checkpoint_save.argtypes = [p, i64, i32, ck, p]

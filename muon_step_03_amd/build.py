@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(HERE, "libmuon.so")
 
 SOURCES = ["muon_abi.hip", "k_elementwise.hip", "k_ns_bf16.hip", "k_ns_f32.hip", "k_adamw.hip",
            "layer_abi.hip", "k_layernorm.hip", "k_checkpoint.hip", "k_weight_grad.hip",
-           "adamw8_abi.hip", "k_adamw8.hip", "linear_abi.hip", "k_linear.hip", "k_weight8.hip"]
+           "adamw8_abi.hip", "k_adamw8.hip", "linear_abi.hip", "k_linear.hip",
+           "k_linear_stream.hip", "k_linear_few.hip", "k_weight8.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

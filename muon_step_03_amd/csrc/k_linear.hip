@@ -11,144 +11,34 @@
 // two k, in an order of k that is the same for both operands.  The weight of the
 // input gradient runs along n: its tile holds rows of k, which bf16 reads with
 // transposing LDS reads and float32 by the element.
+//
+// Tiles of 64 x 64 (four steps on their way to LDS) while those of 128 x 128 (two
+// blocks per CU, a step ahead) would not fill the chip: bound by latency there,
+// then by the loads from the L2.  Measured on one MI355X: bf16 input gradient of
+// 49152 tokens, 64 x 1408 x 512, uneven, 128 x 128: 89 us (790 TFLOP/s); 1023 tokens
+// of 7 x 777 x 1001, no row on 16 bytes, 64 x 64: 16.5 us; 1024 tokens of 1024 x 1024
+// 10.3 us.  float32: 16384 tokens of 1024 x 1024 261 us, 131 TFLOP/s of the 143 that
+// a large library product reaches; 2049 tokens of 7 x 1001 x 777 51 us.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "lds_tiles.h"
-#include "linear_internal.h"
+#include "linear_device.h"
 
 namespace muon {
 namespace {
-
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-
-constexpr int ROWB = 128;    // bytes of k per row and step
-constexpr int SIDE = MUON_WEIGHT_BLOCK;
-
-int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
-__device__ __forceinline__ int cdiv_d(int x, int m) { return (x + m - 1) / m; }
-
-// Chunk c of row r lies at chunk c ^ swz(r): the 16 lanes that a 16-byte read
-// serves at once (four quads of every other quad) then use all 64 banks once.
-__device__ __forceinline__ int swz(int r) { return (r >> 1 & 1) | (r >> 3 & 3) << 1; }
-
-// ------------------------------------------------------------ tiles and tokens
-// The tokens [begin, end) of matrix e (e < 0: of none, whose outputs are zero),
-// and this block's tile among theirs.
-struct Place {
-  int e, begin, end;
-  int tm, tn;
-};
-
-// Tile number -> tile row and column: groups of 8 tile rows, columns first
-// within a group, so that 32 consecutive tiles (an XCD's compute units) share
-// their operands.
-__device__ __forceinline__ void place_tile(int tile, int tiles_m, int tiles_n, int& ti, int& tj) {
-  const int group = tile / (8 * tiles_n), r = tile - group * 8 * tiles_n;
-  const int rows = tiles_m - group * 8 < 8 ? tiles_m - group * 8 : 8;
-  tj = r / rows;
-  ti = group * 8 + r - tj * rows;
-}
-
-// Number of block b among `total`: the hardware deals blocks to the 8 XCDs in
-// turn; XCD x takes a contiguous eighth.
-__device__ __forceinline__ int64_t xcd_order(uint32_t b, uint32_t total) {
-  const uint32_t per = (total + 7) / 8, turn = b >> 3, id = (b & 7) * per + turn;
-  return turn < per && id < total ? int64_t(id) : -1;
-}
-
-// The place of this block.  With offsets, every block finds the bounds itself:
-// segment 0 lies before the first offset, segment s holds matrix s - 1, the last
-// one the tokens behind the last offset.  Offsets are clamped to [0, tokens] and
-// read as the largest so far, so that no place leaves the buffers.  `lds`: 2
-// kLinearMaxSegs + 64 words.
-template <int THREADS>
-__device__ __forceinline__ bool find_place(const Linear& p, int bm, int tiles_n, LDS_AS int* lds,
-                                           Place& out) {
-  const int t = threadIdx.x, T = int(p.tokens);
-  if (!p.offsets) {
-    const int tiles_m = cdiv_d(T, bm);
-    const int64_t id = xcd_order(blockIdx.x, uint32_t(tiles_m) * tiles_n);
-    if (id < 0) return false;
-    out.e = out.begin = 0;
-    out.end = T;
-    place_tile(int(id), tiles_m, tiles_n, out.tm, out.tn);
-    return true;
-  }
-  constexpr int WAVES = THREADS / 64;
-  const int lane = t & 63, wave = t >> 6, segs = p.count + 2;
-  LDS_AS int *ends = lds, *firsts = lds + kLinearMaxSegs, *wave_top = firsts + kLinearMaxSegs,
-             *wave_sum = wave_top + 16, *found = wave_sum + 16;
-  int top = 0, tiles = 0;   // of the segments before this group
-  for (int base = 0; base < segs; base += THREADS) {
-    const int s = base + t;
-    int hi = 0;
-    if (s <= p.count) {
-      const int64_t v = p.offsets[s];
-      hi = int(v < 0 ? 0 : v > T ? T : v);
-    } else if (s < segs) {
-      hi = T;
-    }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(hi, off, 64);
-      if (lane >= off && o > hi) hi = o;
-    }
-    if (lane == 63) wave_top[wave] = hi;
-    __syncthreads();
-    int before = top;
-    for (int w = 0; w < wave; ++w) before = before > wave_top[w] ? before : wave_top[w];
-    hi = hi > before ? hi : before;
-    int lo = __shfl_up(hi, 1, 64);
-    if (lane == 0) lo = before;
-    const int n = s < segs ? cdiv_d(hi - lo, bm) : 0;
-    int sum = n;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(sum, off, 64);
-      if (lane >= off) sum += o;
-    }
-    if (lane == 63) wave_sum[wave] = sum;
-    __syncthreads();
-    int first = tiles + sum - n;
-    for (int w = 0; w < wave; ++w) first += wave_sum[w];
-    if (s < segs) {
-      ends[s] = hi;
-      firsts[s] = first;
-    }
-    for (int w = 0; w < WAVES; ++w) {
-      top = top > wave_top[w] ? top : wave_top[w];
-      tiles += wave_sum[w];
-    }
-    __syncthreads();
-  }
-  const int64_t id = xcd_order(blockIdx.x, uint32_t(tiles) * tiles_n);
-  if (id < 0) return false;
-  for (int s = t; s < segs; s += THREADS) {
-    const int64_t a = int64_t(firsts[s]) * tiles_n,
-                  b = int64_t(s + 1 < segs ? firsts[s + 1] : tiles) * tiles_n;
-    if (id >= a && id < b) *found = s;
-  }
-  __syncthreads();
-  const int s = __builtin_amdgcn_readfirstlane(*found);
-  const int first = __builtin_amdgcn_readfirstlane(firsts[s]);
-  const int next = __builtin_amdgcn_readfirstlane(s + 1 < segs ? firsts[s + 1] : tiles);
-  out.e = s > p.count ? -1 : s - 1;
-  out.begin = __builtin_amdgcn_readfirstlane(s > 0 ? ends[s - 1] : 0);
-  out.end = __builtin_amdgcn_readfirstlane(ends[s]);
-  place_tile(int(id - int64_t(first) * tiles_n), next - first, tiles_n, out.tm, out.tn);
-  __syncthreads();      // the tiles overwrite what was read here
-  return true;
-}
 
 // ---------------------------------------------------------------- the epilogue
 // Writes a wave's 32 MT tokens (from t0) x 32 NT outputs (from n0) through a
 // window of LDS of its own, 32 tokens at a time, so that lanes store whole runs
 // of a row.  Lane l, register 4 g + i of a 32 x 32 block holds token l % 32,
-// output 8 g + 4 (l / 32) + i.
+// output 8 g + 4 (l / 32) + i.  STREAM: the L2 need not keep them, as for calls that
+// fill the chip with the larger tiles (49152 tokens of 64 x 1408 x 512, input
+// gradient: 110 -> 94 us).
 template <int NT>
 constexpr int window_bytes() { return 32 * (32 * NT + 4) * 4; }
-template <int MT, int NT>
+template <int MT, int NT, bool STREAM>
 __device__ __forceinline__ void store_tile(const Linear& p, int t0, int end, int n0,
                                            const f32x16_t (&acc)[MT][NT], LDS_AS char* window,
                                            int lane) {
@@ -180,7 +70,7 @@ __device__ __forceinline__ void store_tile(const Linear& p, int t0, int end, int
             for (int j = 0; j < 4; ++j) v[i + j] = x[j];
           }
           using T = typename RowVec<decltype(bf16)::value>::T;
-          store_vec<decltype(bf16)::value>(static_cast<T*>(p.y) + int64_t(t) * p.n + n, 0, p.n - n, v);
+          store_vec<decltype(bf16)::value, STREAM>(static_cast<T*>(p.y) + int64_t(t) * p.n + n, 0, p.n - n, v);
         }
       }
     };
@@ -193,32 +83,36 @@ __device__ __forceinline__ void store_tile(const Linear& p, int t0, int end, int
 }
 
 // ------------------------------------------------------------------- the tiles
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
 struct Shape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;   // tokens, outputs, waves
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int MT = BM / WM / 32, NT = BN / WN / 32;     // 32 x 32 blocks per wave
+  static constexpr int STAGES = STAGES_;   // steps in LDS, loaded straight there
+  static constexpr int AHEAD = BM == 64 ? 4 : 2;                 // steps in registers otherwise
 };
-using Tile128 = Shape<128, 128, 2, 2>;
-using Tile256 = Shape<256, 256, 2, 4>;
+using Tile64 = Shape<64, 64, 2, 2, 4>;
+using Tile128 = Shape<128, 128, 2, 2, 2>;
 
 template <LinearType TYPE>
 constexpr int elem_bytes() { return TYPE == LIN_BF16 ? 2 : TYPE == LIN_F32 ? 4 : 1; }
 
-// ACROSS: the weight's rows are k (dx = dy W).  DIRECT: both operands' rows
-// start on 16 bytes and hold whole chunks, so that they go straight to LDS;
-// otherwise they pass through registers, where what follows a row's end becomes
-// zero.
-template <LinearType TYPE, bool ACROSS, bool DIRECT, class S>
+// ACROSS: the weight's rows are k (dx = dy W).  How operands reach LDS: straight,
+// where the rows of both start on 16 bytes and hold whole chunks; otherwise
+// through registers, where what follows a row's end becomes zero; rows shorter
+// than a chunk by elements.
+enum LinearPath { DIRECTLY, BY_VECTORS, BY_ELEMENTS };
+template <LinearType TYPE, bool ACROSS, LinearPath PATH, class S>
 __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(const Linear p, int tiles_n) {
   constexpr int ES = elem_bytes<TYPE>(), BK = ROWB / ES;
   constexpr int BM = S::BM, BN = S::BN, MT = S::MT, NT = S::NT, THREADS = S::THREADS;
-  constexpr bool E4M3 = TYPE >= LIN_E4M3;
+  constexpr bool E4M3 = TYPE >= LIN_E4M3, DIRECT = PATH == DIRECTLY, TINY = PATH == BY_ELEMENTS;
   static_assert(!(E4M3 && ACROSS), "8-bit weights are kept both ways");
   constexpr int X_BYTES = BM * ROWB, W_BYTES = BN * ROWB;
   constexpr int XS_BYTES = E4M3 ? S::NW * 256 : 0;        // x scales of a step
   constexpr int STAGE = X_BYTES + W_BYTES + XS_BYTES;
-  constexpr int WS_AT = 2 * STAGE, WS_BYTES = E4M3 ? BN / SIDE * (MUON_MAX_DIM / SIDE) : 0;
+  constexpr int STAGES = DIRECT ? S::STAGES : 2;
+  constexpr int WS_AT = STAGES * STAGE, WS_BYTES = E4M3 ? (BN + SIDE - 1) / SIDE * (MUON_MAX_DIM / SIDE) : 0;
   constexpr int LDS_BYTES = WS_AT + WS_BYTES;
   static_assert(LDS_BYTES <= (S::NW == 8 ? 160 : 80) * 1024, "LDS");
   static_assert(S::NW * window_bytes<NT>() <= LDS_BYTES, "the epilogue's windows");
@@ -226,8 +120,13 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
   LDS_AS char* smem = (LDS_AS char*)smem_raw;
   const uint32_t smem_base = uint32_t(reinterpret_cast<uintptr_t>(smem));
 
-  Place at;
-  if (!find_place<THREADS>(p, BM, tiles_n, (LDS_AS int*)smem, at)) return;
+  Bounds bounds{};
+  bounds.tiles = cdiv_d(int(p.tokens), BM);
+  if (p.offsets) bounds = find_bounds<THREADS, true>(p, BM, (LDS_AS int*)smem);
+  const int64_t id = xcd_order(blockIdx.x, uint32_t(bounds.tiles) * tiles_n);
+  if (id < 0) return;
+  const Place at = place_of(p, bounds, BM, tiles_n, int(id));
+  __syncthreads();      // the tiles overwrite what was read here
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
@@ -256,7 +155,7 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
   auto x_at = [&](int i) { return DIRECT ? (wave * XI + i) * 64 + lane : i * THREADS + t; };
   auto w_at = [&](int i) { return DIRECT ? (wave * WI + i) * 64 + lane : i * THREADS + t; };
   // where chunk c of row k of a w across lies
-  auto w_swz = [](int k) { return TYPE == LIN_BF16 ? gswz(k) : (k >> 2 & 1) << 3; };
+  auto w_swz = [](int k) { return TYPE == LIN_BF16 ? swz_across<BN>(k) : (k >> 2 & 1) << 3; };
 
   // ---- loads straight to LDS
   uint32_t x_off[XI], w_off[WI];
@@ -278,6 +177,7 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
     }
   }
   // x scales: a word per row and step.
+  constexpr int LOADS = XI + WI + (E4M3 ? 1 : 0);   // per wave and step
   const uint32_t xs_row = (wave * 64 + lane) % BM;
   const uint32_t xs_off = E4M3 ? uint32_t(int(xs_row) < rows_x ? int(xs_row) : rows_x - 1) * uint32_t(p.xs_pitch) : 0;
   const char* xs = E4M3 ? reinterpret_cast<const char*>(p.x_scale) + int64_t(t0) * p.xs_pitch : nullptr;
@@ -328,45 +228,71 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
     }
   };
 
-  // ---- loads through registers (float32 and bf16)
+  // ---- loads through registers (float32 and bf16).  A vector that crosses a row's
+  // end, or lies behind it, is loaded from the row's last elements and shifted down
+  // when it is written, with zeros behind them: a load that no branch guards, which
+  // nothing has to wait for before (elements loaded one by one in the last step
+  // took half of the time of 1000 tokens).
+  constexpr int AHEAD = DIRECT ? 1 : S::AHEAD;
   using R = RowVec<TYPE == LIN_BF16>;
-  u32x4_t xr[DIRECT ? 1 : XI], wr[DIRECT ? 1 : WI];
-  auto load = [&](int k) __attribute__((always_inline)) {
+  constexpr int N = R::N;
+  u32x4_t xq[AHEAD][DIRECT ? 1 : XI], wq[AHEAD][DIRECT ? 1 : WI];
+  auto load = [&](auto slot, int k) __attribute__((always_inline)) {
     if constexpr (!DIRECT) {
-      const bool whole = k < steps - 1 || last_k == BK;
+      constexpr bool BF16 = TYPE == LIN_BF16;
+      using T = typename R::T;
+      auto& xr = xq[decltype(slot)::value];
+      auto& wr = wq[decltype(slot)::value];
+      auto along = [&](const char* rows, int64_t ld, int r, int c) __attribute__((always_inline)) {
+        const T* row = reinterpret_cast<const T*>(rows + r * ld);
+        const int at = k * BK + c * N;
+        if constexpr (TINY) {
+          return load_raw<BF16>(row, at, p.k);
+        } else {
+          const typename R::Raw v = *reinterpret_cast<const typename R::Raw*>(row + min(at, p.k - N));
+          return u32x4_t{v[0], v[1], v[2], v[3]};
+        }
+      };
 #pragma unroll
-      for (int i = 0; i < XI; ++i) {
-        const int r = x_at(i) / 8, c = x_at(i) % 8;
-        const char* row = x + int64_t(r < rows_x ? r : rows_x - 1) * p.ldx + int64_t(k) * ROWB;
-        if (whole)
-          xr[i] = load_raw<TYPE == LIN_BF16, true>(row, c * R::N, BK);
-        else
-          xr[i] = load_raw<TYPE == LIN_BF16>(row, c * R::N, last_k);
-      }
+      for (int i = 0; i < XI; ++i)
+        xr[i] = along(x, p.ldx, min(x_at(i) / 8, rows_x - 1), x_at(i) % 8);
 #pragma unroll
       for (int i = 0; i < WI; ++i) {
         if constexpr (ACROSS) {
-          const int kr = w_at(i) / WPR, c = w_at(i) % WPR;
-          const char* row = w + (int64_t(k) * BK + kr) * p.ldw;
-          if (!whole && kr >= last_k)
-            wr[i] = u32x4_t{0, 0, 0, 0};
-          else if (rows_w == BN)
-            wr[i] = load_raw<TYPE == LIN_BF16, true>(row, c * R::N, BN);
-          else
-            wr[i] = load_raw<TYPE == LIN_BF16>(row, c * R::N, rows_w);
+          const T* row = reinterpret_cast<const T*>(static_cast<const char*>(p.W) + at.e * p.w_stride +
+                                                    min(k * BK + w_at(i) / WPR, p.k - 1) * p.ldw);
+          const int col = n0 + w_at(i) % WPR * N;
+          if constexpr (TINY) {
+            wr[i] = load_raw<BF16>(row, col, p.n);
+          } else {
+            const typename R::Raw v = *reinterpret_cast<const typename R::Raw*>(row + min(col, p.n - N));
+            wr[i] = u32x4_t{v[0], v[1], v[2], v[3]};
+          }
         } else {
-          const int r = w_at(i) / 8, c = w_at(i) % 8;
-          const char* row = w + int64_t(r < rows_w ? r : rows_w - 1) * p.ldw + int64_t(k) * ROWB;
-          if (whole)
-            wr[i] = load_raw<TYPE == LIN_BF16, true>(row, c * R::N, BK);
-          else
-            wr[i] = load_raw<TYPE == LIN_BF16>(row, c * R::N, last_k);
+          wr[i] = along(w, p.ldw, min(w_at(i) / 8, rows_w - 1), w_at(i) % 8);
         }
       }
     }
   };
-  auto write = [&](int buf) __attribute__((always_inline)) {
+  auto write = [&](auto slot, int buf, int k) __attribute__((always_inline)) {
     if constexpr (!DIRECT) {
+      constexpr bool BF16 = TYPE == LIN_BF16;
+      auto& xr = xq[decltype(slot)::value];
+      auto& wr = wq[decltype(slot)::value];
+      if (k == steps - 1 && last_k < BK) {
+#pragma unroll
+        for (int i = 0; i < XI; ++i)
+          if (!TINY) shift_down<BF16>(xr[i], max(x_at(i) % 8 * N + N - last_k, 0));
+#pragma unroll
+        for (int i = 0; i < WI; ++i) {
+          if (!ACROSS && !TINY) shift_down<BF16>(wr[i], max(w_at(i) % 8 * N + N - last_k, 0));
+          if (ACROSS && w_at(i) / WPR >= last_k) wr[i] = u32x4_t{0, 0, 0, 0};
+        }
+      }
+      if (ACROSS && rows_w < BN && !TINY) {
+#pragma unroll
+        for (int i = 0; i < WI; ++i) shift_down<BF16>(wr[i], max(n0 + w_at(i) % WPR * N - (p.n - N), 0));
+      }
       LDS_AS char* s = smem + buf * STAGE;
 #pragma unroll
       for (int i = 0; i < XI; ++i) {
@@ -391,7 +317,7 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
     if constexpr (!ACROSS) {
       return frag(tile, row0, s);
     } else if constexpr (TYPE == LIN_BF16) {
-      return __builtin_bit_cast(u32x4_t, lds_frag_xT<BN>(tile, 16 * s, row0, lane));
+      return __builtin_bit_cast(u32x4_t, frag_across<BN>(tile, 16 * s, row0, lane));
     } else {
       const int n = row0 + (lane & 31), k = 4 * (2 * s + (lane >> 5));
       u32x4_t v;
@@ -414,28 +340,14 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
       const uint32_t wsc = *reinterpret_cast<const LDS_AS uint8_t*>(smem + WS_AT + wr0 / SIDE * (MUON_MAX_DIM / SIDE) + k);
       static_assert(SIDE % (NT * 32) == 0, "a wave's outputs share a scale");
       if constexpr (TYPE == LIN_E4M3_EXACT) {
-        // a chunk of 16 as two of bf16, exact: the conversion multiplies by 2^e
-        // (255, a marked block, by NaN)
-        auto wide = [&](u32x4_t q, uint32_t byte, bf16x8_t (&o)[2]) {
-          const float up = __uint_as_float(byte << 23);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const u32x4_t v = {
-                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * h], up, false)),
-                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * h], up, true)),
-                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * h + 1], up, false)),
-                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * h + 1], up, true))};
-            o[h] = __builtin_bit_cast(bf16x8_t, v);
-          }
-        };
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           bf16x8_t xf[MT][2], wf[NT][2];
           // both chunks of a fragment (one per half of the lanes) are of block c
 #pragma unroll
-          for (int a = 0; a < MT; ++a) wide(frag(s, xr0 + a * 32, c), sx[a] >> (8 * c) & 0xff, xf[a]);
+          for (int a = 0; a < MT; ++a) widen(frag(s, xr0 + a * 32, c), sx[a] >> (8 * c) & 0xff, xf[a]);
 #pragma unroll
-          for (int b = 0; b < NT; ++b) wide(frag(sw, wr0 + b * 32, c), wsc, wf[b]);
+          for (int b = 0; b < NT; ++b) widen(frag(sw, wr0 + b * 32, c), wsc, wf[b]);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -473,28 +385,38 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
           }
       }
     } else {
+      // small bf16 tiles read a whole step first, for a wave has too few products in
+      // a chunk to wait for the next one's reads behind them (1023 tokens of 777 x
+      // 1001: 17.3 -> 16.4 us)
+      constexpr int FIRST = MT * NT == 1 && TYPE == LIN_BF16 ? 4 : 1;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        u32x4_t xf[MT], wf[NT];
+      for (int c0 = 0; c0 < 4; c0 += FIRST) {
+        u32x4_t xf[FIRST][MT], wf[FIRST][NT];
 #pragma unroll
-        for (int a = 0; a < MT; ++a) xf[a] = frag(s, xr0 + a * 32, c);
+        for (int c = 0; c < FIRST; ++c) {
 #pragma unroll
-        for (int b = 0; b < NT; ++b) wf[b] = frag_w(sw, wr0 + b * 32, c);
+          for (int a = 0; a < MT; ++a) xf[c][a] = frag(s, xr0 + a * 32, c0 + c);
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+          for (int b = 0; b < NT; ++b) wf[c][b] = frag_w(sw, wr0 + b * 32, c0 + c);
+        }
+        if constexpr (FIRST > 1) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int b = 0; b < NT; ++b) {
-            if constexpr (TYPE == LIN_BF16) {
-              acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, wf[b]),
-                                                                  __builtin_bit_cast(bf16x8_t, xf[a]),
-                                                                  acc[a][b], 0, 0, 0);
-            } else {
+        for (int c = 0; c < FIRST; ++c)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(wf[b][i]),
-                                                                 __uint_as_float(xf[a][i]), acc[a][b], 0, 0, 0);
+          for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+              if constexpr (TYPE == LIN_BF16) {
+                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, wf[c][b]),
+                                                                    __builtin_bit_cast(bf16x8_t, xf[c][a]),
+                                                                    acc[a][b], 0, 0, 0);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(wf[c][b][i]),
+                                                                   __uint_as_float(xf[c][a][i]), acc[a][b], 0, 0, 0);
+              }
             }
-          }
       }
     }
   };
@@ -503,81 +425,169 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
     if constexpr (E4M3) {      // the weight's scales, all of k
       const uint8_t* ws = p.w_scale + at.e * p.ws_stride + int64_t(n0 / SIDE) * p.ws_row;
 #pragma unroll
-      for (int b = 0; b < BN / SIDE; ++b)
+      for (int b = 0; b < (BN + SIDE - 1) / SIDE; ++b)
         if (n0 + b * SIDE < p.n)
           for (int k = t; k < steps; k += THREADS)
             *reinterpret_cast<LDS_AS uint8_t*>(smem + WS_AT + b * (MUON_MAX_DIM / SIDE) + k) =
                 ws[b * p.ws_row + k * p.ws_col];
     }
     if constexpr (DIRECT) {
-      issue(std::true_type{}, 0, 0);
+      std::true_type end;
+#pragma unroll
+      for (int k = 0; k < STAGES - 1; ++k)
+        if (k < steps) issue(end, k, k);
+      int buf = 0;
       for (int k = 0; k < steps; ++k) {
-        wait_vmcnt<0>();
+        // step k has come: only the loads of the steps behind it may be on their way
+        const int behind = min(steps - 1 - k, STAGES - 2);
+        if (STAGES == 2 || behind == 0)
+          wait_vmcnt<0>();
+        else if (behind == 1)
+          wait_vmcnt<LOADS>();
+        else
+          wait_vmcnt<2 * LOADS>();
+        static_assert(STAGES == 2 || STAGES == 4, "the waits above");
         asm volatile("" ::: "memory");
-        if (!E4M3 && k == steps - 1 && last_chunks < 8) clear_tail(k & 1);
+        if (!E4M3 && k == steps - 1 && last_chunks < 8) clear_tail(buf);
         block_barrier();
-        if (k + 1 < steps) issue(std::true_type{}, (k + 1) & 1, k + 1);
-        multiply(k & 1, k);
+        if (k + STAGES - 1 < steps) issue(end, (buf + STAGES - 1) % STAGES, k + STAGES - 1);
+        multiply(buf, k);
+        buf = (buf + 1) % STAGES;
       }
     } else {
-      load(0);
-      write(0);
-      for (int k = 0; k < steps; ++k) {
+      // Steps k + 1 .. k + AHEAD are on their way to registers while step k is
+      // multiplied.  Behind the last step that one is loaded again: loads behind a
+      // branch would all be waited for at the next write.
+      auto step = [&](auto slot, int k) __attribute__((always_inline)) {
+        constexpr int I = decltype(slot)::value;
         block_barrier();
-        if (k + 1 < steps) load(k + 1);
+        load(slot, min(k + AHEAD, steps - 1));
         multiply(k & 1, k);
-        if (k + 1 < steps) write((k + 1) & 1);
+        write(std::integral_constant<int, (I + 1) % AHEAD>{}, (k + 1) & 1, k + 1);
+      };
+      std::integral_constant<int, 0> c0;
+      std::integral_constant<int, 1 % AHEAD> c1;
+      std::integral_constant<int, 2 % AHEAD> c2;
+      std::integral_constant<int, 3 % AHEAD> c3;
+      load(c0, 0);
+      load(c1, min(1, steps - 1));
+      if constexpr (AHEAD == 4) {
+        load(c2, min(2, steps - 1));
+        load(c3, min(3, steps - 1));
       }
+      write(c0, 0, 0);
+      int k = 0;
+      for (; k + AHEAD <= steps; k += AHEAD) {
+        step(c0, k);
+        step(c1, k + 1);
+        if constexpr (AHEAD == 4) {
+          step(c2, k + 2);
+          step(c3, k + 3);
+        }
+      }
+      if (k < steps) step(c0, k);
+      if (k + 1 < steps) step(c1, k + 1);
+      if (AHEAD == 4 && k + 2 < steps) step(c2, k + 2);
     }
     block_barrier();
   }
-  store_tile<MT, NT>(p, t0 + wm * MT * 32, at.end, n0 + wn * NT * 32, acc,
+  store_tile<MT, NT, BM == 128>(p, t0 + wm * MT * 32, at.end, n0 + wn * NT * 32, acc,
                      smem + wave * window_bytes<NT>(), lane);
 }
 
-template <LinearType TYPE, bool ACROSS, bool DIRECT, class S>
+template <LinearType TYPE, bool ACROSS, LinearPath PATH, class S>
 hipError_t launch_tiles(const Linear& p, hipStream_t s) {
   const int64_t tiles_n = cdiv(p.n, S::BN);
-  const int64_t tiles_m = p.offsets ? p.tokens / S::BM + p.count + 2 : cdiv(p.tokens, S::BM);
-  hipLaunchKernelGGL((linear_kernel<TYPE, ACROSS, DIRECT, S>), dim3(unsigned(cdiv(tiles_m * tiles_n, 8) * 8)),
+  // of the matrices, only those with tokens have tiles, and the tokens of none
+  const int64_t tiles_m = p.offsets ? p.tokens / S::BM + std::min<int64_t>(p.count + 2, p.tokens)
+                                    : cdiv(p.tokens, S::BM);
+  hipLaunchKernelGGL((linear_kernel<TYPE, ACROSS, PATH, S>), dim3(unsigned(cdiv(tiles_m * tiles_n, 8) * 8)),
                      dim3(S::THREADS), 0, s, p, int(tiles_n));
   return hipGetLastError();
+}
+template <LinearType TYPE, bool ACROSS, LinearPath PATH>
+hipError_t launch_shape(const Linear& p, LinearPlan plan, hipStream_t s) {
+  return plan == LIN_64 ? launch_tiles<TYPE, ACROSS, PATH, Tile64>(p, s)
+                        : launch_tiles<TYPE, ACROSS, PATH, Tile128>(p, s);
+}
+template <LinearType TYPE, bool ACROSS>
+hipError_t launch_path(const Linear& p, LinearPath path, LinearPlan plan, hipStream_t s) {
+  if (path == DIRECTLY) return launch_shape<TYPE, ACROSS, DIRECTLY>(p, plan, s);
+  if (path == BY_VECTORS) return launch_shape<TYPE, ACROSS, BY_VECTORS>(p, plan, s);
+  return launch_tiles<TYPE, ACROSS, BY_ELEMENTS, Tile64>(p, s);
 }
 
 }  // namespace
 
+// Estimates of the tiles of `bm` tokens that a call has: matrices share the tokens
+// evenly, and half of a tile of each lies behind its last token.
+static double tiles_of(int64_t count, int64_t tokens, int64_t n, int bm, int bn) {
+  const double hit = double(std::min(count, std::max<int64_t>(tokens, 1))), each = double(tokens) / hit;
+  return hit * std::max(1.0, each / bm + (count > 1 ? 0.5 : 0.0)) * double(cdiv(n, bn));
+}
+
+// Which kernel, by times measured on one MI355X for 1, 8 and 64 matrices of 1408 x
+// 512 to 5632 x 2048 and 1 to 16384 tokens (microseconds, bf16 unless said).
+static LinearPlan choose(LinearType type, bool across, int64_t count, int64_t tokens, int64_t k, int64_t n) {
+  const double few = tiles_of(count, tokens, n, 16, 16), n64 = tiles_of(count, tokens, n, 64, 64),
+               n128 = tiles_of(count, tokens, n, 128, 128), n256 = tiles_of(count, tokens, n, 256, 256);
+  // Few tokens, while the blocks are all there at once (1 token of 4096 x 1024: 6.0,
+  // tiles of 64 9.5; 64 tokens 12.9 and 9.7).  float32, whose tiles are slow, where
+  // the tokens of a matrix are few (64 matrices of 1408 x 512, 1024 tokens: 57, 65).
+  if (!across && (few <= 768 || (type == LIN_F32 && tokens <= 16 * count))) return LIN_FEW;
+  if (type == LIN_F32) {
+    // bound by the matrix instructions: the fewer products with nothing, a tile of
+    // 128 taking 3.3 times one of 64 (4096 tokens of 64 x 1408 x 512: 102 against 68;
+    // of one 1024 x 1024: 78 against 89)
+    return n128 >= 200 && 3.3 * n128 <= n64 ? LIN_128 : LIN_64;
+  }
+  // Tiles of 64 until those of 128 fill the chip (1024 tokens of 1024 x 1024: 10.3
+  // against 14.9; 4096: 22.7 against 17.7).
+  if (n64 <= 640) return LIN_64;
+  if (type == LIN_E4M3_EXACT) return LIN_128;
+  // Blocks that stay, from two per CU on (16384 tokens of 64 x 1408 x 512: 40 against
+  // 47; across the rows they gain nothing), and their tiles of 256 x 256, which read
+  // half as much, where whole rounds of them do not lose it again (16384 tokens of
+  // 4096 x 1024: 139, of 128 x 128 154; of 1408 x 512: 43 against 35).
+  const double steps = double(k) * (type == LIN_E4M3 ? 1 : 2) / ROWB;
+  const double step256 = type == LIN_E4M3 ? 1.22 : across ? 1.62 : 1.34, step128 = across ? 0.88 : 0.93;
+  const double us256 = std::ceil(n256 / 256) * (step256 * steps + 10),
+               us128 = std::max(1.0, n128 / 512) * (step128 * steps + 3);
+  // (whole steps of k, and rows of outputs of whole 16 bytes)
+  const bool whole = k % (type == LIN_E4M3 ? 128 : 64) == 0 && n % 8 == 0;
+  if (whole && us256 < us128) return LIN_STREAM_256;
+  return whole && n128 >= 512 && !across ? LIN_STREAM_128 : LIN_128;
+}
+
 LinearPlan linear_plan(LinearType type, bool across, int64_t count, int64_t tokens, int64_t k, int64_t n) {
-  if ((tokens / 128 + count + 10) * cdiv(n, 128) >= (int64_t(1) << 24) - 8) return LIN_NONE;
-  if (type == LIN_F32) return LIN_128;
-  return cdiv(tokens, count) >= 512 ? LIN_256 : LIN_128;
+  const LinearPlan plan = choose(type, across, count, tokens, k, n);
+  // the largest grid, with whole turns of the 8 XCDs (rows that do not start on 16
+  // bytes may take tiles of 128 instead of 256)
+  const int64_t side = plan == LIN_FEW ? 16 : plan == LIN_64 ? 64 : 128;
+  return (tokens / side + count + 2) * cdiv(n, side) >= (int64_t(1) << 24) - 8 ? LIN_NONE : plan;
 }
 
 hipError_t launch_linear(const Linear& p, LinearType type, bool across, LinearPlan plan, hipStream_t s) {
-  const int es = type == LIN_BF16 ? 2 : 4;
+  const int es = type == LIN_BF16 ? 2 : 4, vec = 16 / es;
   // whole chunks in both operands' rows, and offsets within a tile in 32 bits
   const bool direct = type >= LIN_E4M3 ||
                       (reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && reinterpret_cast<uintptr_t>(p.W) % 16 == 0 &&
-                       p.ldx % 16 == 0 && p.ldw % 16 == 0 && p.k * es % 16 == 0 && (!across || p.n * es % 16 == 0) &&
+                       p.ldx % 16 == 0 && p.ldw % 16 == 0 && p.k % vec == 0 && (!across || p.n % vec == 0) &&
                        p.ldx <= (1 << 23));
-  if (type == LIN_E4M3_EXACT) return launch_tiles<LIN_E4M3_EXACT, false, true, Tile128>(p, s);
-  if (type == LIN_E4M3)
-    return plan == LIN_256 ? launch_tiles<LIN_E4M3, false, true, Tile256>(p, s)
-                           : launch_tiles<LIN_E4M3, false, true, Tile128>(p, s);
-  if (type == LIN_BF16) {
-    if (plan == LIN_256 && direct)
-      return across ? launch_tiles<LIN_BF16, true, true, Tile256>(p, s)
-                    : launch_tiles<LIN_BF16, false, true, Tile256>(p, s);
-    if (direct)
-      return across ? launch_tiles<LIN_BF16, true, true, Tile128>(p, s)
-                    : launch_tiles<LIN_BF16, false, true, Tile128>(p, s);
-    return across ? launch_tiles<LIN_BF16, true, false, Tile128>(p, s)
-                  : launch_tiles<LIN_BF16, false, false, Tile128>(p, s);
+  const LinearPath path = direct                                       ? DIRECTLY
+                          : p.k >= vec && (!across || p.n >= vec) ? BY_VECTORS
+                                                                       : BY_ELEMENTS;
+  if (plan == LIN_FEW) return launch_linear_few(p, type, s);
+  if ((plan == LIN_STREAM_128 || plan == LIN_STREAM_256) && direct)
+    return launch_linear_stream(p, type, across, plan == LIN_STREAM_256 ? 256 : 128, s);
+  switch (type) {
+    case LIN_E4M3_EXACT: return launch_shape<LIN_E4M3_EXACT, false, DIRECTLY>(p, plan, s);
+    case LIN_E4M3: return launch_shape<LIN_E4M3, false, DIRECTLY>(p, plan, s);
+    case LIN_BF16:
+      return across ? launch_path<LIN_BF16, true>(p, path, plan, s) : launch_path<LIN_BF16, false>(p, path, plan, s);
+    default:
+      return across ? launch_path<LIN_F32, true>(p, path, plan, s) : launch_path<LIN_F32, false>(p, path, plan, s);
   }
-  if (direct)
-    return across ? launch_tiles<LIN_F32, true, true, Tile128>(p, s)
-                  : launch_tiles<LIN_F32, false, true, Tile128>(p, s);
-  return across ? launch_tiles<LIN_F32, true, false, Tile128>(p, s)
-                : launch_tiles<LIN_F32, false, false, Tile128>(p, s);
 }
 
 }  // namespace muon

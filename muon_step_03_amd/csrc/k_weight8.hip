@@ -5,7 +5,8 @@
 //
 // A block of threads takes one block of the weight: read once, its largest
 // magnitude found, converted, written, and written again exchanged through LDS.
-// HBM-bound: 2 (or 4) bytes in and 2 out per element.
+// HBM-bound: 2 (or 4) bytes in and 2 out per element.  Measured on one MI355X: bf16
+// 4096 x 1024 6.7 us.
 #include "linear_internal.h"
 
 namespace muon {

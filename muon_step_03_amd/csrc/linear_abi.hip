@@ -150,6 +150,17 @@ int muon_weight_quantize(const void* W, int dtype, const muon_weight8* out, void
   return launched(launch_weight_quantize(p, dtype == MUON_DTYPE_BF16, s), "weight_quantize", s);
 }
 
+int muon_linear_kernel(int input_grad, int quantized, int64_t count, int64_t tokens, int64_t rows,
+                       int64_t cols, int dtype) {
+  if (!dtype_ok(dtype) || count < 1 || !weight_sizes_ok(count, rows, cols) || !sizes_ok(tokens, cols) || tokens < 1)
+    return -1;
+  const LinearType type = !quantized ? (dtype == MUON_DTYPE_BF16 ? LIN_BF16 : LIN_F32)
+                                     : (dtype == MUON_DTYPE_BF16 ? LIN_E4M3 : LIN_E4M3_EXACT);
+  const LinearPlan plan = input_grad ? linear_plan(type, !quantized, count, tokens, rows, cols)
+                                     : linear_plan(type, false, count, tokens, cols, rows);
+  return plan == LIN_NONE ? -1 : int(plan);
+}
+
 int muon_linear_forward(const void* x, int64_t ldx, int dtype, const void* W, const int64_t* offsets,
                         int64_t count, int64_t tokens, int64_t rows, int64_t cols, void* y,
                         void* stream) {

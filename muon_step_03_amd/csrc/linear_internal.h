@@ -37,9 +37,14 @@ struct Linear {
 constexpr int kLinearMaxCount = MUON_LINEAR_MAX_COUNT;
 constexpr int kLinearMaxSegs = kLinearMaxCount + 2;
 
-// How a call is computed.
-enum LinearPlan { LIN_FEW, LIN_128, LIN_256, LIN_NONE };
+// How a call is computed.  FEW to STREAM_256 are MUON_LINEAR_* of muon.h.
+enum LinearPlan { LIN_FEW, LIN_64, LIN_128, LIN_STREAM_128, LIN_STREAM_256, LIN_NONE };
 LinearPlan linear_plan(LinearType type, bool across, int64_t count, int64_t tokens, int64_t k, int64_t n);
+// The kernel whose blocks stay, tiles of 128 x 128 or 256 x 256: bf16 and e4m3 in
+// whole steps of k, rows of outputs in whole 16 bytes.
+hipError_t launch_linear_stream(const Linear& p, LinearType type, bool across, int side, hipStream_t s);
+// The kernel for few tokens, along a weight's rows: 16 outputs of 16 tokens a block.
+hipError_t launch_linear_few(const Linear& p, LinearType type, hipStream_t s);
 hipError_t launch_linear(const Linear& p, LinearType type, bool across, LinearPlan plan, hipStream_t s);
 
 // Weights in 8 bits.

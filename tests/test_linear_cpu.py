@@ -147,3 +147,14 @@ def test_oracle_of_ragged_products():
     assert np.allclose(y[1:4], x[1:4] @ W[0].T) and np.allclose(y[4:], x[4:] @ W[2].T)
     assert np.allclose(lin.input_grad(y, W, [1, 4, 3, 12])[5], y[5] @ W[2])
     assert lin.bounds([-3, 100, 5], 9).tolist() == [0, 9, 9]
+
+
+@built
+def test_kernel_choice_refuses_what_calls_refuse():
+    k = _lib.lib().muon_linear_kernel
+    assert k(0, 0, 1, 1, 4096, 1024, BF16) == _lib.MUON_LINEAR_FEW
+    assert k(1, 0, 64, 49152, 1408, 512, BF16) in range(5)
+    for bad in ((0, 0, 0, 1, 64, 64, 0), (0, 0, 1025, 1, 64, 64, 0), (0, 0, 1, 0, 64, 64, 0),
+                (0, 0, 1, 1, 0, 64, 0), (0, 0, 1, 1, 64, BIG + 1, 0), (0, 0, 1, 1, 64, 64, 2),
+                (0, 0, 1, 1 << 30, BIG, BIG, 0)):
+        assert k(*bad) == -1
