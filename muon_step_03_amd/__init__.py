@@ -1,6 +1,6 @@
-"""Muon optimizer step (with the AdamW step of the hybrid optimizer and the
-layer operators that make their gradients) for MI355X (gfx950): HIP kernels
-behind a C ABI.
+"""Muon optimizer step (with the AdamW step of the hybrid optimizer, the layer
+operators that make their gradients and the products of linear layers) for
+MI355X (gfx950): HIP kernels behind a C ABI.
 
 The HIP library (libmuon.so, built in-tree by ``muon_step_03_amd.build``) is
 loaded on first use; without it every entry point raises.
@@ -16,5 +16,5 @@ from .layer_ops import (  # noqa: F401
     ActCheckpoint, LayerNormOut, checkpoint_restore, checkpoint_save, layernorm_backward,
     layernorm_forward, layernorm_workspace_bytes, weight_grad, weight_grad_workspace_bytes,
 )
-from .layers import layer_norm, linear  # noqa: F401
+from .layers import expert_linear, layer_norm, linear  # noqa: F401
 from .linear_ops import Weight8, linear_forward, linear_input_grad, weight_quantize  # noqa: F401

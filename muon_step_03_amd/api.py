@@ -613,13 +613,15 @@ def adamw8_moments(states: Sequence[AdamwState8], dtype: torch.dtype = torch.flo
         total += s.n
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the states on {device}")
-    arr, count = _c_array(_lib.Adamw8State, [s._c for s in states])
     code = dtype_code(dtype)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        m = torch.empty(total, dtype=dtype, device=device)
-        r = torch.empty_like(m)
-        st = _lib.lib().muon_adamw_byte_moments(arr, count, m.data_ptr(), r.data_ptr(), code,
-                                            _stream_handle(None))
+    if stream is not None or torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device), torch.cuda.stream(stream):
+            return adamw8_moments(states, dtype)
+    arr, count = _c_array(_lib.Adamw8State, [s._c for s in states])
+    m = torch.empty(total, dtype=dtype, device=device)
+    r = torch.empty_like(m)
+    st = _lib.lib().muon_adamw_byte_moments(arr, count, m.data_ptr(), r.data_ptr(), code,
+                                            torch._C._cuda_getCurrentRawStream(device.index))
     _check(st, "muon_adamw_byte_moments")
     return m, r
 

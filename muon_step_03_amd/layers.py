@@ -1,11 +1,12 @@
-"""Differentiable layers over the layer operators: ``layer_norm`` and
-``linear`` for models whose parameters ``HybridMuonAdamW`` steps.
+"""Differentiable layers over the layer operators: ``layer_norm``, ``linear`` and
+``expert_linear`` for models whose parameters ``HybridMuonAdamW`` steps.
 
 What they keep for the backward pass is a checkpoint in 8 bits where asked
-for: the norm's input, the linear layer's input.  Norm, checkpoints and weight
-gradients run in the library's kernels; the forward product ``x W^T`` and the
-input gradient ``dy W`` are PyTorch's plain matrix products.  Both run outside
-autocast, in the types of their arguments.
+for: the norm's input, the linear layers' input.  Norm, checkpoints, weight
+gradients, the products of experts and all products in 8 bits run in the
+library's kernels; the products of ``linear`` in the tensors' own type are
+PyTorch's plain matrix products.  All run outside autocast, in the types of
+their arguments.
 
 A backward pass may be captured into a graph when the forward pass it belongs
 to is captured with it and no other autograd graph of the same parameters is
@@ -21,6 +22,7 @@ from torch.autograd.function import once_differentiable
 
 from .layer_ops import (ActCheckpoint, checkpoint_save, layernorm_backward, layernorm_forward,
                         weight_grad)
+from .linear_ops import Weight8, linear_forward, linear_input_grad, weight_quantize
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
@@ -99,21 +101,125 @@ class _Linear(torch.autograd.Function):
         return dx, dW, None, None
 
 
-def linear(x, W, keep: Union[str, ActCheckpoint] = "e4m3"):
+class _ExpertLinear(torch.autograd.Function):
+    """x [tokens, cols] by the experts' weights in x's own type."""
+
+    @staticmethod
+    def forward(ctx, x, W, offsets, q, scale):
+        ctx.save_for_backward(W, offsets, q, scale)
+        return linear_forward(_rows(x), W, offsets=offsets)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        W, offsets, q, scale = ctx.saved_tensors
+        dx = dW = None
+        dy = _rows(dy)
+        if ctx.needs_input_grad[0]:
+            dx = linear_input_grad(dy, W, offsets=offsets)
+        if ctx.needs_input_grad[1]:
+            dW = weight_grad(dy, ActCheckpoint(q, scale, W.shape[2]), offsets=offsets, dtype=W.dtype)
+        return dx, dW, None, None, None
+
+
+class _Linear8(torch.autograd.Function):
+    """Both products from 8 bits, dense or per expert; x and W only carry the
+    gradients, which pass the rounding as if it were not there."""
+
+    @staticmethod
+    def forward(ctx, x, W, offsets, q, scale, wq, wq_t, ws):
+        ctx.save_for_backward(offsets, q, scale, wq, wq_t, ws)
+        ctx.shape, ctx.dtypes = x.shape, (x.dtype, W.dtype)
+        y = linear_forward(ActCheckpoint(q, scale, x.shape[-1]), Weight8(wq, wq_t, ws), offsets=offsets,
+                           dtype=x.dtype)
+        return y.view(*x.shape[:-1], y.shape[1])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        offsets, q, scale, *w8 = ctx.saved_tensors
+        dx = dW = None
+        dy = _rows(dy)
+        if ctx.needs_input_grad[0]:
+            dx = linear_input_grad(checkpoint_save(dy, "e4m3"), Weight8(*w8), offsets=offsets,
+                                   dtype=ctx.dtypes[0]).view(ctx.shape)
+        if ctx.needs_input_grad[1]:
+            dW = weight_grad(dy, ActCheckpoint(q, scale, ctx.shape[-1]), offsets=offsets,
+                             dtype=ctx.dtypes[1])
+        return dx, dW, *(None,) * 6
+
+
+def _check_keep(keep, x, products):
+    """The checkpoint of x that ``keep`` gives or names."""
+    if isinstance(keep, ActCheckpoint):
+        if keep.shape != (x.numel() // max(1, x.shape[-1]), x.shape[-1]) or keep.device != x.device:
+            raise ValueError(f"keep is {keep}, x has shape {tuple(x.shape)} on {x.device}")
+    if products is not None and (keep.format if isinstance(keep, ActCheckpoint) else keep) != "e4m3":
+        raise ValueError("products in 8 bits read the checkpoint of x: keep must be e4m3")
+    return keep if isinstance(keep, ActCheckpoint) else checkpoint_save(_rows(x.detach()), keep)
+
+
+def _check_products(products, W):
+    """The 8-bit weight that ``products`` gives or asks for."""
+    if isinstance(products, Weight8):
+        if products.shape != tuple(W.shape) or products.device != W.device:
+            raise ValueError(f"products is {products}, W has shape {tuple(W.shape)} on {W.device}")
+        return products
+    if products != "e4m3":
+        raise ValueError(f"products must be None, 'e4m3' or a Weight8, not {products!r}")
+    return weight_quantize(W.detach().contiguous())
+
+
+def _linear8(x, W, offsets, keep, products):
+    ck, w8 = _check_keep(keep, x, products), _check_products(products, W)
+    return _Linear8.apply(x, W, offsets, ck.q, ck.scale, w8.q, w8.q_t, w8.scale)
+
+
+def linear(x, W, keep: Union[str, ActCheckpoint] = "e4m3", *,
+           products: Union[None, str, Weight8] = None):
     """``x W^T`` for x [..., cols] and a 2-D weight W [rows, cols] of the same
     type, keeping x for the weight gradient in 8 bits: in the format ``keep``,
-    or as the checkpoint of x given (one that :func:`layer_norm` returned)."""
+    or as the checkpoint of x given (one that :func:`layer_norm` returned).
+
+    products: None multiplies x and W as they are.  "e4m3" multiplies the
+    checkpoint of x with W in 8 bits (scales for 32 columns and for 128 x 128
+    elements), and in the backward pass dy, in 8 bits too, with the same W; a
+    :class:`Weight8` of W, made once after each optimizer step, spares the
+    micro-batches the quantizing."""
     if W.ndim != 2:
         raise ValueError(f"W must be 2-D, it has {W.ndim} dims")
     if x.dtype != W.dtype:
         raise TypeError(f"x has dtype {x.dtype}, W {W.dtype}")
     if x.shape[-1] != W.shape[1]:
         raise ValueError(f"x has {x.shape[-1]} columns, W {W.shape[1]}")
+    if products is not None:
+        return _linear8(x, W, None, keep, products)
     if not (torch.is_grad_enabled() and W.requires_grad):
         return _product(x, W.t())      # no weight gradient: nothing is kept
-    if isinstance(keep, ActCheckpoint):
-        if keep.shape != (x.numel() // max(1, x.shape[-1]), x.shape[-1]) or keep.device != x.device:
-            raise ValueError(f"keep is {keep}, x has shape {tuple(x.shape)} on {x.device}")
-    else:
-        keep = checkpoint_save(_rows(x.detach()), keep)
+    keep = _check_keep(keep, x, None)
     return _Linear.apply(x, W, keep.q, keep.scale)
+
+
+def expert_linear(x, W, offsets, keep: Union[str, ActCheckpoint] = "e4m3", *,
+                  products: Union[None, str, Weight8] = None):
+    """``x[t] W[e]^T`` for x [tokens, cols] and the experts' weights W [count,
+    rows, cols] of the same type; the tokens [offsets[e], offsets[e + 1]) are
+    expert e's (offsets: int64 GPU tensor of count + 1 running totals, read on
+    the device only).  Tokens of no expert give zeros and get zero gradients.
+    keep, products: as for :func:`linear`."""
+    if x.ndim != 2 or W.ndim != 3:
+        raise ValueError(f"x must be [tokens, cols] and W [count, rows, cols], not {tuple(x.shape)} "
+                         f"and {tuple(W.shape)}")
+    if x.dtype != W.dtype:
+        raise TypeError(f"x has dtype {x.dtype}, W {W.dtype}")
+    if x.shape[1] != W.shape[2]:
+        raise ValueError(f"x has {x.shape[1]} columns, W {W.shape[2]}")
+    if products is not None:
+        return _linear8(x, W, offsets, keep, products)
+    if not (torch.is_grad_enabled() and (x.requires_grad or W.requires_grad)):
+        return linear_forward(_rows(x), W, offsets=offsets)
+    q = scale = None
+    if W.requires_grad:
+        keep = _check_keep(keep, x, None)
+        q, scale = keep.q, keep.scale
+    return _ExpertLinear.apply(x, W, offsets, q, scale)

@@ -30,7 +30,7 @@ class Weight8:
     column blocks] of 128 x 128 elements.  An element stands for
     ``q * 2^(scale - 127)``."""
 
-    __slots__ = ("q", "q_t", "scale", "shape", "device", "_c")
+    __slots__ = ("_q", "_q_t", "_scale", "_buffer", "shape", "device", "_c")
 
     def __init__(self, q: torch.Tensor, q_t: torch.Tensor, scale: torch.Tensor):
         for name, t, dtype in (("q", q, torch.float8_e4m3fn), ("q_t", q_t, torch.float8_e4m3fn),
@@ -41,18 +41,19 @@ class Weight8:
                 raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if q.ndim not in (2, 3) or q_t.ndim != q.ndim:
             raise ValueError("q and q_t must be a matrix or a stack of matrices each")
-        lead, rows, cols = tuple(q.shape[:-2]), q.shape[-2], q_t.shape[-2]
-        blocks = [_lib.weight_pitch(n) // _lib.MUON_WEIGHT_BLOCK for n in (rows, cols)]
-        for name, t, shape in (("q", q, (rows, _lib.weight_pitch(cols))),
-                               ("q_t", q_t, (cols, _lib.weight_pitch(rows))),
-                               ("scale", scale, tuple(blocks))):
-            if tuple(t.shape) != lead + shape or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError(f"{name} must be a contiguous GPU tensor of shape {lead + shape} "
+        *lead, rows, qp = q.shape
+        cols, tp = q_t.shape[-2:]
+        pr, pc = (rows + 127) // 128, (cols + 127) // 128
+        device = q.device
+        for name, t, shape in (("q", q, [*lead, rows, 128 * pc]), ("q_t", q_t, [*lead, cols, 128 * pr]),
+                               ("scale", scale, [*lead, pr, pc])):
+            if list(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"{name} must be a contiguous GPU tensor of shape {tuple(shape)} "
                                  f"for weights of {rows} x {cols}, got {tuple(t.shape)}")
-            if t.device != q.device:
-                raise ValueError(f"{name} is on {t.device}, q on {q.device}")
-        self.q, self.q_t, self.scale = q, q_t, scale
-        self.shape, self.device = lead + (rows, cols), q.device
+            if t.device != device:
+                raise ValueError(f"{name} is on {t.device}, q on {device}")
+        self._q, self._q_t, self._scale, self._buffer = q, q_t, scale, None
+        self.shape, self.device = (*lead, rows, cols), device
         self._c = _lib.Weight8(q.data_ptr(), q_t.data_ptr(), scale.data_ptr(),
                                lead[0] if lead else 1, rows, cols)
 
@@ -63,10 +64,48 @@ class Weight8:
         if len(shape) not in (2, 3) or min(shape[-2:]) < 1 or min(shape) < 0:
             raise ValueError(f"a weight has the shape (rows, cols) or (count, rows, cols), not {shape}")
         lead, (rows, cols) = shape[:-2], shape[-2:]
-        pr, pc = _lib.weight_pitch(rows), _lib.weight_pitch(cols)
-        new = lambda s, dtype: torch.empty(lead + s, dtype=dtype, device=device)  # noqa: E731
-        return cls(new((rows, pc), torch.float8_e4m3fn), new((cols, pr), torch.float8_e4m3fn),
-                   new((pr // 128, pc // 128), torch.uint8))
+        pr, pc = (rows + 127) // 128, (cols + 127) // 128
+        n = lead[0] if lead else 1
+        # one allocation for the three, each from a multiple of 128 bytes on; the
+        # tensors are made when asked for
+        a, b = n * rows * pc * 128, n * cols * pr * 128
+        w = cls.__new__(cls)
+        w._buffer = torch.empty(a + b + n * pr * pc, dtype=torch.uint8, device=device)
+        if not w._buffer.is_cuda:
+            raise ValueError(f"a Weight8 must be on a GPU, not on {w._buffer.device}")
+        w._q = w._q_t = w._scale = None
+        w.shape, w.device = (*lead, rows, cols), w._buffer.device
+        at = w._buffer.data_ptr()
+        w._c = _lib.Weight8(at, at + a, at + a + b, n, rows, cols)
+        return w
+
+    def _split(self):
+        *lead, rows, cols = self.shape
+        pr, pc = (rows + 127) // 128, (cols + 127) // 128
+        n = lead[0] if lead else 1
+        a, b = n * rows * pc * 128, n * cols * pr * 128
+        buf = self._buffer
+        self._q = buf[:a].view(torch.float8_e4m3fn).view(*lead, rows, 128 * pc)
+        self._q_t = buf[a:a + b].view(torch.float8_e4m3fn).view(*lead, cols, 128 * pr)
+        self._scale = buf[a + b:].view(*lead, pr, pc)
+
+    @property
+    def q(self) -> torch.Tensor:
+        if self._q is None:
+            self._split()
+        return self._q
+
+    @property
+    def q_t(self) -> torch.Tensor:
+        if self._q_t is None:
+            self._split()
+        return self._q_t
+
+    @property
+    def scale(self) -> torch.Tensor:
+        if self._scale is None:
+            self._split()
+        return self._scale
 
     def __reduce__(self):      # copies and pickles have tensors of their own
         return Weight8, (self.q, self.q_t, self.scale)
@@ -96,7 +135,7 @@ def weight_quantize(W: torch.Tensor, *, out: Optional[Weight8] = None, stream=No
                                          _raw_stream(W.device.index))
     _check(st, "muon_weight_quantize")
     if given is not None:
-        _wrote(given.q, given.q_t, given.scale)
+        _wrote(*((given._q, given._q_t, given._scale) if given._buffer is None else (given._buffer,)))
     return out
 
 
