@@ -9,9 +9,9 @@
 // vectors of 8 consecutive elements, so 4 neighbouring lanes hold a block and
 // find its largest magnitude with two lane exchanges; all loads of a thread
 // are issued before its arithmetic.  HBM-bound, with the vector units close
-// behind: 77 M elements of bf16 (GPT-160M's embedding and head) take 152 us on
-// one MI355X, 5.1 TB/s where a 1 GiB copy moves 5.45; reading both moments
-// back 79 us (5.9).
+// behind: 77 M elements of bf16 (GPT-160M's embedding and head) take 148 us on
+// one MI355X, 5.3 TB/s where a 1 GiB copy moves 5.45; reading both moments
+// back 76 us (6.1).
 #include <type_traits>
 
 #include "adamw8_internal.h"

@@ -237,7 +237,7 @@ def test_captured_training_pass(products):
     def both():
         X = x.detach().requires_grad_()
         z = M.expert_linear(torch.relu(M.expert_linear(X, W, o, products=products)), V, o, products=products)
-        return (z, *torch.autograd.grad(z, (X, W, V), torch.ones_like(z)))
+        return (z.detach(), *torch.autograd.grad(z, (X, W, V), torch.ones_like(z)))
 
     both()
     torch.cuda.synchronize()

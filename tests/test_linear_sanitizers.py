@@ -15,6 +15,8 @@ def test_linear_validation_under_asan_and_ubsan(tmp_path):
     for src, flags in ((os.path.join(CSRC, "linear_abi.hip"), ["-O1", "-g"] + SAN),
                        (os.path.join(ROOT, "tests", "linear_validation_driver.cpp"), ["-O1", "-g"] + SAN),
                        (os.path.join(CSRC, "k_linear.hip"), ["-O1"]),
+                       (os.path.join(CSRC, "k_linear_stream.hip"), ["-O1"]),
+                       (os.path.join(CSRC, "k_linear_few.hip"), ["-O1"]),
                        (os.path.join(CSRC, "k_weight8.hip"), ["-O1"]),
                        (os.path.join(CSRC, "muon_abi.hip"), ["-O1"]),
                        (os.path.join(CSRC, "k_elementwise.hip"), ["-O1"]),
