@@ -660,8 +660,12 @@ class AdamWStep:
         self.step_count = 0
 
     def _seed(self, i):
-        """Of parameter i in the current step: any two differ."""
-        return (self.seed + 0x9e3779b1 * (self.step_count * len(self.entries) + i)) & 0xffffffff
+        """Of parameter i in the current step: any two differ, by no fixed step (the
+        elements' numbers enter their random bits by a fixed one)."""
+        n = self.step_count * len(self.entries) + i & 0xffffffff
+        n = (n ^ n >> 16) * 0x45d9f3b & 0xffffffff
+        n = (n ^ n >> 16) * 0x45d9f3b & 0xffffffff
+        return (self.seed + (n ^ n >> 16)) & 0xffffffff
 
     @torch.no_grad()
     def step(self):

@@ -158,3 +158,17 @@ def test_random_bits_differ_between_elements_seeds_and_halves():
     for x in (a >> 16, a & 0xffff):
         assert abs(x.mean() / 65535 - 0.5) < 5 / np.sqrt(12 * x.size)
     assert abs(np.corrcoef(a >> 16, a & 0xffff)[0, 1]) < 0.02
+
+
+def test_random_bits_of_parameters_and_steps_share_no_run():
+    """The optimizer's seeds of 64 parameters and steps: no tensor's random bits are
+    another's, shifted.  2^18 draws of 2^32 numbers repeat 2^36 / 2^33 = 8 times by
+    chance; a shifted run would repeat some 4000 times."""
+    opt = object.__new__(M.AdamWStep)
+    opt.seed, opt.entries = 3, [None] * 16
+    seeds = []
+    for opt.step_count in range(1, 5):
+        seeds += [opt._seed(i) for i in range(16)]
+    assert len(set(seeds)) == 64 and all(0 <= s < 1 << 32 for s in seeds)
+    bits = np.concatenate([ao.random_bits(4096, s) for s in seeds])
+    assert bits.size - np.unique(bits).size < 64
