@@ -158,3 +158,14 @@ def test_kernel_choice_refuses_what_calls_refuse():
                 (0, 0, 1, 1, 0, 64, 0), (0, 0, 1, 1, 64, BIG + 1, 0), (0, 0, 1, 1, 64, 64, 2),
                 (0, 0, 1, 1 << 30, BIG, BIG, 0)):
         assert k(*bad) == -1
+
+
+def test_grids_of_short_rows_count_their_smaller_tiles():
+    """Rows shorter than 16 bytes are computed in tiles of 64 whatever the choice
+    for longer ones is: four times the blocks."""
+    k = _lib.lib().muon_linear_kernel
+    tokens = 1 << 24
+    assert k(0, 0, 1, tokens, 4096, 8, BF16) == _lib.MUON_LINEAR_TILES_128
+    assert k(0, 0, 1, tokens, 4096, 7, BF16) == -1
+    assert k(1, 0, 1, tokens, 7, 4096, BF16) == -1
+    assert k(0, 0, 1, tokens // 2, 4096, 7, BF16) >= 0

@@ -367,3 +367,21 @@ def test_outputs_that_autograd_kept_are_noticed():
     M.linear_forward(x, W, out=z.detach())
     with pytest.raises(RuntimeError, match="modified"):
         keep.backward()
+
+
+@pytest.mark.parametrize("tokens", [3, 200])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_subnormal_operands(dtype, tokens):
+    """x of 1 .. 63 steps of 2^-133 (bf16's smallest number), W a power of two: sums of
+    one product each are exact."""
+    g = torch.Generator().manual_seed(2)
+    x = torch.zeros(tokens, 96)
+    at = torch.randint(0, 96, (tokens,), generator=g)
+    x[torch.arange(tokens), at] = torch.randint(1, 64, (tokens,), generator=g).float() * 2.0 ** -133
+    x = x.to(dtype).to(DEV)
+    W = torch.full((80, 96), 2.0 ** 20, dtype=dtype, device=DEV)
+    want = (f64(x).sum(1) * 2.0 ** 20)[:, None] * np.ones(80)
+    assert (want > 0).all()
+    assert np.array_equal(f64(M.linear_forward(x, W)), want)
+    V = torch.full((96, 80), 2.0 ** 20, dtype=dtype, device=DEV)
+    assert np.array_equal(f64(M.linear_input_grad(x, V)), want)
