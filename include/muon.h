@@ -302,10 +302,10 @@ int muon_adamw_step_grouped(const muon_adamw_tensor* tensors, int64_t count, int
  *           of one call.
  *  Sizes    0 <= n <= MUON_ADAMW8_MAX_ELEMENTS; n == 0 skips the tensor.
  *  Scalars, stream, errors  as for muon_adamw_step_grouped; one launch per
- *           MUON_ADAMW8_TENSORS_PER_LAUNCH tensors.
+ *           MUON_ADAMW8_TENSORS_PER_LAUNCH 56tensors.
  */
 #define MUON_ADAMW8_MAX_ELEMENTS (((int64_t)1) << 35)
-#define MUON_ADAMW8_TENSORS_PER_LAUNCH 48
+#define MUON_ADAMW8_TENSORS_PER_LAUNCH 56
 
 typedef struct muon_adamw8_state {
   void* m_q;        /* e4m3, n bytes up to a multiple of 32 */

@@ -32,7 +32,7 @@ MUON_GROUPS_PER_LAUNCH = 8
 MUON_ADAMW_MAX_ELEMENTS = 1 << 40
 MUON_ADAMW_TENSORS_PER_LAUNCH = 32
 MUON_ADAMW8_MAX_ELEMENTS = 1 << 35
-MUON_ADAMW8_TENSORS_PER_LAUNCH = 48
+MUON_ADAMW8_TENSORS_PER_LAUNCH = 56
 MUON_NOALLOC_WORKSPACE_BYTES = 64 << 20
 MUON_MAX_TOKENS = 1 << 30
 MUON_CKPT_BLOCK = 32

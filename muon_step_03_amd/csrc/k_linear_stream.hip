@@ -14,7 +14,7 @@
 //   read units 1 .. of step s          multiply 0 .. of step s
 //   step s + 1 has come: barrier       (all have read step s: its place is free)
 //   read unit 0 of step s + 1, issue   multiply the last unit
-//   the loads of step s + STAGES
+//   the loads of step s + 2
 //
 // Measured on one MI355X: e4m3, 256 x 256, 16384 tokens of 4096 x 1024 across
 // (k = 4096) 64 us, 2150 TFLOP/s; of 8 x 5632 x 2048, uneven, 194 (1950); bf16,
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(256, PER_CU) void linear_stream_kernel(const Linear
   // again, which nothing reads.
   const int64_t w_step = ACROSS ? BK * p.ldw : ROWB;
   auto issue_end = [&]() __attribute__((always_inline)) {
-    load_buf = load_buf == STAGES - 1 ? 0 : load_buf + 1;
+    load_buf ^= 1;
     if (load_k + 1 < steps) {
       ++load_k;
       x += ROWB;
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(256, PER_CU) void linear_stream_kernel(const Linear
         }
       y += int64_t(32) * p.n * 2;
     }
-    return whole ? 1 : 0;
+    return whole;
   };
 
   load_tile();
@@ -358,7 +358,7 @@ __global__ __launch_bounds__(256, PER_CU) void linear_stream_kernel(const Linear
   for (int i = 0; i < READS; ++i) read_one(f0, 0, 0, i);
   if constexpr (E4M3) read_scales(0);
   int buf = 0;
-  int stored1 = 0, stored2 = 0;       // whether a tile's stores ended the step before, the one before that
+  bool stored = false;       // whether a tile's stores ended the step before
   std::integral_constant<int, 0> u0;
   std::integral_constant<int, 1> u1;
   std::integral_constant<int, 2> u2;
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(256, PER_CU) void linear_stream_kernel(const Linear
   for (int number = 0; number < tiles; ++number) {
     if constexpr (!FIRST) clear();
     for (int k = 0; k < steps; ++k) {
-      const int next = buf == STAGES - 1 ? 0 : buf + 1;
+      const int next = buf ^ 1;
       if constexpr (E4M3) {
 #pragma unroll
         for (int a = 0; a < MT; ++a) sx[a] = sx_next[a] >> (8 * (lane >> 5));
@@ -385,18 +385,13 @@ __global__ __launch_bounds__(256, PER_CU) void linear_stream_kernel(const Linear
         run_unit(f1, u1, f0, buf, 2, only_reads, std::false_type{});
         run_unit(f0, u2, f1, buf, 3, only_reads, std::false_type{});
       }
-      // the next step has come: behind it, the loads of the steps after it and the
-      // stores of tiles that ended since may be on their way
-      constexpr int BEHIND = (STAGES - 2) * LOADS;
-      const int stored = stored1 + (STAGES == 3 ? stored2 : 0);
-      if (stored == 0)
-        wait_vmcnt<BEHIND>();
-      else if (stored == 1)
-        wait_vmcnt<BEHIND + STORES>();
+      // the next step has come: behind it, the stores of a tile that ended since may
+      // be on their way
+      if (stored)
+        wait_vmcnt<STORES>();
       else
-        wait_vmcnt<BEHIND + (STAGES - 1) * STORES>();
-      stored2 = stored1;
-      stored1 = 0;
+        wait_vmcnt<0>();
+      stored = false;
       asm volatile("" ::: "memory");
       block_barrier();
       if constexpr (E4M3) {
@@ -410,7 +405,7 @@ __global__ __launch_bounds__(256, PER_CU) void linear_stream_kernel(const Linear
       issue_end();
       buf = next;
     }
-    stored1 = store(number);
+    stored = store(number);
   }
   wait_vmcnt<0>();      // loads to LDS that nothing waited for
 }

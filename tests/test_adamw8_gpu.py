@@ -125,7 +125,7 @@ def test_unaligned_parameters(dtype, shift):
 
 
 def test_grouped_equals_single_and_moments():
-    """100 tensors (three launches), each with its own lr, decay and seed, some
+    """100 tensors (80 not empty: two launches), each with its own lr, decay and seed, some
     empty: bits of one call per tensor; the moments come back one behind the
     other, exactly."""
     sizes = [1, 0, 64, 777, 4096, 5000, 12345, 33, 0, 8192] * 10
@@ -334,4 +334,4 @@ def test_gpu_front_end_refusals():
         M.AdamwState8(st.r_q, st.m_scale, st.r_q, st.r_scale, 10)
     with pytest.raises(M.MuonError):      # the same buffer twice
         M.adamw8_step(P, P, st, lr=0.1, step=1)
-    assert _lib.MUON_ADAMW8_TENSORS_PER_LAUNCH == 48
+    assert _lib.MUON_ADAMW8_TENSORS_PER_LAUNCH == 56
