@@ -44,6 +44,7 @@ __device__ __forceinline__ void store_tile(const Linear& p, int t0, int end, int
                                            int lane) {
   constexpr int PITCH = 32 * NT + 4;
   LDS_AS float* w = (LDS_AS float*)window;
+  const bool lines = whole_lines(p);
 #pragma unroll
   for (int a = 0; a < MT; ++a) {
 #pragma unroll
@@ -70,7 +71,11 @@ __device__ __forceinline__ void store_tile(const Linear& p, int t0, int end, int
             for (int j = 0; j < 4; ++j) v[i + j] = x[j];
           }
           using T = typename RowVec<decltype(bf16)::value>::T;
-          store_vec<decltype(bf16)::value, STREAM>(static_cast<T*>(p.y) + int64_t(t) * p.n + n, 0, p.n - n, v);
+          T* y = static_cast<T*>(p.y) + int64_t(t) * p.n + n;
+          if (STREAM && lines)
+            store_vec<decltype(bf16)::value, true>(y, 0, p.n - n, v);
+          else
+            store_vec<decltype(bf16)::value, false>(y, 0, p.n - n, v);
         }
       }
     };
@@ -548,7 +553,7 @@ static LinearPlan choose(LinearType type, bool across, int64_t count, int64_t to
   // Blocks that stay, from two per CU on (16384 tokens of 64 x 1408 x 512: 40 against
   // 47; across the rows they gain nothing), and their tiles of 256 x 256, which read
   // half as much, where whole rounds of them do not lose it again (16384 tokens of
-  // 4096 x 1024: 139, of 128 x 128 154; of 1408 x 512: 43 against 35).
+  // 4096 x 2048: 227, of 128 x 128 255; of 1408 x 512: 36 against 30).
   const double steps = double(k) * (type == LIN_E4M3 ? 1 : 2) / ROWB;
   const double step256 = type == LIN_E4M3 ? 1.22 : across ? 1.62 : 1.34, step128 = across ? 0.88 : 0.93;
   const double us256 = std::ceil(n256 / 256) * (step256 * steps + 10),

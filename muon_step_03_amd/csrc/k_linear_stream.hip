@@ -16,13 +16,18 @@
 //   read unit 0 of step s + 1, issue   multiply the last unit
 //   the loads of step s + 2
 //
+// Outputs are stored in whole lines of 128 bytes past the L2 (16384 tokens of 4096 x
+// 1024, e4m3, k = 1024: 86 us with 32 bytes of a row at a time, 78 so; 49152 of 64 x
+// 1408 x 512, bf16: 118, 105).
+//
 // Measured on one MI355X: e4m3, 256 x 256, 16384 tokens of 4096 x 1024 across
-// (k = 4096) 64 us, 2150 TFLOP/s; of 8 x 5632 x 2048, uneven, 194 (1950); bf16,
-// 16384 tokens of 4096 x 1024 139 (990; PyTorch's library product of these widths
-// reaches 900 to 1050).  128 x 128: 49152 tokens of 64 x 1408 x 512, uneven, 119
-// us, of which the instructions alone take 58, the loads 75 (every step waits for
-// the L2, one step ahead being all that LDS holds) and the stores, which loads
-// behind them wait for, the rest.
+// (k = 4096) 64 us, 2150 TFLOP/s; of 8 x 5632 x 2048, uneven, 191 (1980); k = 1024 78
+// (1760), of which 30 are stores: loads behind them wait for them, so that they do
+// not overlap with the next tile.  bf16, 16384 tokens of 4096 x 1024 131 (1050;
+// PyTorch's library product of these widths reaches 900 to 1050).  128 x 128: 49152
+// tokens of 64 x 1408 x 512, uneven, 105 us in a row, of which the instructions alone
+// take 58 and the loads 75 (every step waits for the L2, one step ahead being all
+// that LDS holds).
 #include <algorithm>
 #include <type_traits>
 
@@ -308,38 +313,66 @@ __global__ __launch_bounds__(256, PER_CU) void linear_stream_kernel(const Linear
     pin();
   };
 
-  // ---- a tile's outputs, from the registers.  Lane l, register 4 g + i of a 32
-  // x 32 block holds token l % 32, output 8 g + 4 (l / 32) + i; lanes exchange
-  // halves of two g, so that each stores 16 bytes.  Returns whether every lane
-  // took part in all the stores, which then count as loads in flight do.
+  // ---- a tile's outputs, from the registers, in whole lines of 128 bytes.  Lane
+  // l, register 4 g + i of a 32 x 32 block holds token l % 32, output 8 g + 4 (l /
+  // 32) + i.  The halves of the wave exchange parts of two blocks, so that a lane
+  // has all 32 outputs of a token in one of them, four chunks of 16 bytes; then
+  // four neighbouring lanes exchange chunks, so that they hold the four of one
+  // token, and of the next one, .., which they store side by side.  Returns whether
+  // every lane took part in all the stores, which then count as loads in flight do.
   constexpr int STORES = MT * NT * 2;
   auto store = [&](int number) __attribute__((always_inline)) {
     const Tile at = tile_at(number);
     const int t0 = at.t0 + wm * MT * 32, n0 = at.n0 + wn * NT * 32;
     const bool whole = at.t0 + BM <= at.end && at.n0 + BN <= p.n;
-    const int ln = fresh(lane);
-    const int rows = at.end - t0 - (ln & 31), cols = p.n - n0 - 8 * (ln >> 5);   // that are left
-    char* y = static_cast<char*>(p.y) + (int64_t(t0 + (ln & 31)) * p.n + n0 + 8 * (ln >> 5)) * 2;
+    const int ln = fresh(lane), row = ln & 28, col = 32 * (ln >> 5) + 8 * (ln & 3);
+    const int rows = at.end - t0 - row, cols = p.n - n0 - col;   // that are left
+    char* y = static_cast<char*>(p.y) + (int64_t(t0 + row) * p.n + n0 + col) * 2;
+    const int64_t pitch = int64_t(p.n) * 2;
+    const bool lines = whole_lines(p);
+    const bool odd1 = ln & 1, odd2 = ln & 2;
+    // chunk `lo` of the lanes with the bit and `hi` of those without change places
+    auto exchange = [](u32x4_t& lo, u32x4_t& hi, bool bit, auto perm) __attribute__((always_inline)) {
 #pragma unroll
-    for (int a = 0; a < MT; ++a) {
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t out = bit ? lo[i] : hi[i];
+        const uint32_t in = __builtin_amdgcn_mov_dpp(out, decltype(perm)::value, 0xf, 0xf, true);
+        lo[i] = bit ? in : lo[i];
+        hi[i] = bit ? hi[i] : in;
+      }
+    };
+    const std::integral_constant<int, 0xb1> next1;   // lanes 1 0 3 2
+    const std::integral_constant<int, 0x4e> next2;   // lanes 2 3 0 1
 #pragma unroll
-      for (int b = 0; b < NT; ++b)
+    for (int a = 0; a < MT; ++a)
 #pragma unroll
-        for (int g = 0; g < 4; g += 2) {
-          uint32_t lo[2], hi[2];
+      for (int b = 0; b < NT; b += 2) {
+        u32x4_t c[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t u = f2bf2(acc[a][b][4 * g + 2 * i], acc[a][b][4 * g + 2 * i + 1]);
-            const uint32_t v = f2bf2(acc[a][b][4 * g + 4 + 2 * i], acc[a][b][4 * g + 4 + 2 * i + 1]);
-            const auto r = __builtin_amdgcn_permlane32_swap(u, v, false, false);
-            lo[i] = r[0];
-            hi[i] = r[1];
+            const auto r = __builtin_amdgcn_permlane32_swap(
+                f2bf2(acc[a][b][4 * g + 2 * i], acc[a][b][4 * g + 2 * i + 1]),
+                f2bf2(acc[a][b + 1][4 * g + 2 * i], acc[a][b + 1][4 * g + 2 * i + 1]), false, false);
+            c[g][i] = r[0];
+            c[g][2 + i] = r[1];
           }
-          if (whole || (a * 32 < rows && b * 32 + 8 * g < cols))
-            *reinterpret_cast<RowVec<true>::Raw*>(y + (b * 32 + 8 * g) * 2) = RowVec<true>::Raw{lo[0], lo[1], hi[0], hi[1]};
-        }
-      y += int64_t(32) * p.n * 2;
-    }
+        exchange(c[0], c[1], odd1, next1);
+        exchange(c[2], c[3], odd1, next1);
+        exchange(c[0], c[2], odd2, next2);
+        exchange(c[1], c[3], odd2, next2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (whole || (a * 32 + i < rows && b * 32 < cols)) {
+            const RowVec<true>::Raw v = {c[i][0], c[i][1], c[i][2], c[i][3]};
+            auto to = reinterpret_cast<RowVec<true>::Raw*>(y + (a * 32 + i) * pitch + b * 64);
+            if (lines)
+              __builtin_nontemporal_store(v, to);
+            else
+              *to = v;
+          }
+      }
     return whole;
   };
 

@@ -148,3 +148,19 @@ def test_more_than_2_to_the_32_outputs():
         bound = (cols + 9) * U * mag
         bound = bound + HALF[BF16] * (want.abs() + bound)
         assert float(((y[pick].double() - want).abs() - bound).max()) <= 0
+
+
+@pytest.mark.parametrize("which,across,tokens,rows,cols", [(S128, False, 4100, 2048, 128), (S256, False, 4000, 4096, 4096),
+                                                           (T128, True, 8200, 64, 1024)])
+@pytest.mark.parametrize("at", [8, 5])
+def test_outputs_that_begin_inside_a_line(which, across, tokens, rows, cols, at):
+    """Lines of 128 bytes are stored past the L2, parts of lines through it: the same
+    bits, and what lies before and behind stays as it was."""
+    assert kernel(across, False, 1, tokens, rows, cols, BF16) == which
+    W, x = draw(rows, cols, dtype=BF16, seed=1), draw(tokens, rows if across else cols, dtype=BF16, seed=2)
+    fn = M.linear_input_grad if across else M.linear_forward
+    want = fn(x, W)
+    buf = torch.full((want.numel() + 64,), 7.0, dtype=BF16, device=DEV)
+    out = buf[at:at + want.numel()].view(want.shape)
+    assert torch.equal(fn(x, W, out=out), want)
+    assert bool((buf[:at] == 7).all()) and bool((buf[at + want.numel():] == 7).all())
