@@ -504,9 +504,11 @@ class AdamwState8:
     """Both moments of a tensor of ``n`` elements in 8 bits (``include/muon.h``,
     "State format"): ``m_q`` (float8_e4m3fn) and ``r_q`` (uint8) hold n bytes up
     to a multiple of 32, ``m_scale`` and ``r_scale`` (uint8) one byte per 32
-    elements.  m_q stands for the first moment, r_q for the root of the second."""
+    elements.  m_q stands for the first moment, r_q for the root of the second.
+    The tensors are those that the state was made of and cannot be replaced: a
+    saved state is copied into them (``copy_``), or a new one made of it."""
 
-    __slots__ = ("m_q", "m_scale", "r_q", "r_scale", "n", "device", "_c")
+    __slots__ = ("_m_q", "_m_scale", "_r_q", "_r_scale", "_n", "_device", "_c")
 
     def __init__(self, m_q, m_scale, r_q, r_scale, n: int):
         n = int(n)
@@ -520,8 +522,8 @@ class AdamwState8:
             _check_flat(name, t, numel, dtype)
             if t.device != m_q.device:
                 raise ValueError(f"{name} is on {t.device}, m_q on {m_q.device}")
-        self.m_q, self.m_scale, self.r_q, self.r_scale, self.n = m_q, m_scale, r_q, r_scale, n
-        self.device = m_q.device
+        self._m_q, self._m_scale, self._r_q, self._r_scale, self._n = m_q, m_scale, r_q, r_scale, n
+        self._device = m_q.device
         self._c = _lib.Adamw8State(m_q.data_ptr(), m_scale.data_ptr(), r_q.data_ptr(),
                                    r_scale.data_ptr(), n)
 
@@ -534,8 +536,32 @@ class AdamwState8:
         return cls(buf[:size].view(torch.float8_e4m3fn), buf[2 * size:2 * size + blocks],
                    buf[size:2 * size], buf[2 * size + blocks:], n)
 
-    def __reduce__(self):      # copies and pickles have tensors of their own
+    def __reduce__(self):      # deep copies and pickles have tensors of their own
         return AdamwState8, (self.m_q, self.m_scale, self.r_q, self.r_scale, self.n)
+
+    @property
+    def m_q(self) -> torch.Tensor:
+        return self._m_q
+
+    @property
+    def m_scale(self) -> torch.Tensor:
+        return self._m_scale
+
+    @property
+    def r_q(self) -> torch.Tensor:
+        return self._r_q
+
+    @property
+    def r_scale(self) -> torch.Tensor:
+        return self._r_scale
+
+    @property
+    def n(self) -> int:
+        return self._n
+
+    @property
+    def device(self) -> torch.device:
+        return self._device
 
     @property
     def nbytes(self) -> int:

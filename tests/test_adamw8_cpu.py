@@ -172,3 +172,11 @@ def test_random_bits_of_parameters_and_steps_share_no_run():
     assert len(set(seeds)) == 64 and all(0 <= s < 1 << 32 for s in seeds)
     bits = np.concatenate([ao.random_bits(4096, s) for s in seeds])
     assert bits.size - np.unique(bits).size < 64
+
+
+@pytest.mark.parametrize("field", ["m_q", "m_scale", "r_q", "r_scale", "n", "device"])
+def test_a_states_fields_are_not_assigned(field):
+    """The library steps the tensors that a state was made of: another one put in
+    their place would be neither read nor kept alive."""
+    with pytest.raises(AttributeError):
+        setattr(object.__new__(M.AdamwState8), field, torch.zeros(32))

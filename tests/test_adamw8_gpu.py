@@ -335,3 +335,29 @@ def test_gpu_front_end_refusals():
     with pytest.raises(M.MuonError):      # the same buffer twice
         M.adamw8_step(P, P, st, lr=0.1, step=1)
     assert _lib.MUON_ADAMW8_TENSORS_PER_LAUNCH == 56
+
+
+def test_restoring_a_state():
+    """A state takes a saved one's values into its tensors, or a new state is made
+    of the saved tensors; both go on as the saved one does.  Assignment is refused;
+    a shallow copy shares the tensors, a deep one has its own."""
+    n = 1000
+    P, G = draw(n, torch.float32, 1)
+    st = M.AdamwState8.zeros(n, DEV)
+    M.adamw8_step(P, G, st, lr=0.01, step=1, seed=1)
+    saved = [t.clone() for t in (st.m_q, st.m_scale, st.r_q, st.r_scale)]
+    deep, shallow, p = copy.deepcopy(st), copy.copy(st), P.clone()
+    M.adamw8_step(P, G, st, lr=0.01, step=2, seed=2)
+    want = values(st)
+    filled, made = M.AdamwState8.zeros(n, DEV), M.AdamwState8(*saved, n)
+    for name, t in zip(("m_q", "m_scale", "r_q", "r_scale"), saved):
+        with pytest.raises(AttributeError):
+            setattr(filled, name, t)
+        getattr(filled, name).copy_(t)
+    for state in (filled, made, deep):
+        q = p.clone()
+        M.adamw8_step(q, G, state, lr=0.01, step=2, seed=2)
+        assert torch.equal(q, P)
+        assert all(np.array_equal(a, b) for a, b in zip(values(state), want))
+    assert shallow.m_q.data_ptr() == st.m_q.data_ptr() and shallow.n == n and shallow.device == st.device
+    assert all(np.array_equal(a, b) for a, b in zip(values(shallow), want))
