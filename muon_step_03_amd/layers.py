@@ -6,7 +6,8 @@ for: the norm's input, the linear layers' input.  Norm, checkpoints, weight
 gradients, the products of experts and all products in 8 bits run in the
 library's kernels; the products of ``linear`` in the tensors' own type are
 PyTorch's plain matrix products.  All run outside autocast, in the types of
-their arguments.
+their arguments.  What runs in the library has no forward-mode derivative: a
+tangent that reaches it raises.
 
 A backward pass may be captured into a graph when the forward pass it belongs
 to is captured with it and no other autograd graph of the same parameters is
@@ -216,10 +217,8 @@ def expert_linear(x, W, offsets, keep: Union[str, ActCheckpoint] = "e4m3", *,
         raise ValueError(f"x has {x.shape[1]} columns, W {W.shape[2]}")
     if products is not None:
         return _linear8(x, W, offsets, keep, products)
-    if not (torch.is_grad_enabled() and (x.requires_grad or W.requires_grad)):
-        return linear_forward(_rows(x), W, offsets=offsets)
     q = scale = None
-    if W.requires_grad:
+    if torch.is_grad_enabled() and W.requires_grad:
         keep = _check_keep(keep, x, None)
         q, scale = keep.q, keep.scale
     return _ExpertLinear.apply(x, W, offsets, q, scale)
