@@ -107,6 +107,14 @@ def check_stats(stats, n_matrices: int, device=None) -> None:
         raise ValueError(f"stats is on {stats.device}, the weights on {device}")
 
 
+def _wrote(*given):
+    """Tells autograd that tensors it did not make were written: a backward
+    pass that kept one of them then raises, as after PyTorch's own writes."""
+    for t in given:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -180,6 +188,7 @@ def muon_step(W, G, M, *, lr=0.02, momentum=0.95, weight_decay=0.1, ns_steps=5,
         *_scalars(dt, lr, momentum, weight_decay, ns_steps, ns_coefficients, variant, scale),
         _ptr(ws), ws.numel() * ws.element_size(), _ptr(stats), _stream_handle(stream))
     _check(st, "muon_step")
+    _wrote(W, M)
     if workspace is None:
         _keep_for_stream(stream, ws)
     return W, M
@@ -222,6 +231,7 @@ def muon_step_batched(Ws, Gs, Ms, *, lr=0.02, momentum=0.95, weight_decay=0.1, n
                   variant, scale),
         _ptr(ws), ws.numel() * ws.element_size(), _ptr(stats), _stream_handle(stream))
     _check(st, "muon_step_batched")
+    _wrote(*Ws, *Ms)
     _keep_for_stream(stream, *(tables if own_tables else ()), ws if workspace is None else None)
 
 
@@ -295,7 +305,9 @@ def muon_step_grouped(groups: Sequence[_lib.MuonGroup], dtype: torch.dtype, *, l
                       workspace=None, stats=None, stream=None, device=None):
     """One Muon step over several shape groups (a whole model) in one launch
     sequence.  Build groups with :func:`stacked_group` / :func:`table_group`;
-    the caller keeps the tensors they point to alive."""
+    the caller keeps the tensors they point to alive.  A group holds addresses
+    only: autograd is not told that the weights were written (the calls and
+    optimizers that are given the tensors themselves tell it)."""
     groups = list(groups)
     need = workspace_bytes_grouped(groups, dtype)
     if device is None:
@@ -434,6 +446,7 @@ class MuonStep:
             st = None if stats is None else \
                 stats[offset * _lib.MUON_STATS_PER_MATRIX:(offset + n) * _lib.MUON_STATS_PER_MATRIX]
             muon_step_grouped(groups, dtype, workspace=ws, stats=st, device=ws.device, **self.hp)
+            _wrote(*(self.params[i] for idx in shapes.values() for i in idx))
             offset += n
 
 
@@ -484,12 +497,14 @@ def adamw_step(P, G, m, v, *, lr, step, betas=AUX_BETAS, eps=AUX_EPS,
                                     float(betas[0]), float(betas[1]), float(eps),
                                     t.weight_decay, int(step), _stream_handle(stream))
     _check(st, "muon_adamw_step")
+    _wrote(P, m, v)
 
 
 def adamw_step_grouped(tensors: Sequence[_lib.AdamwTensor], dtype: torch.dtype, *, step,
                        betas=AUX_BETAS, eps=AUX_EPS, stream=None):
     """One AdamW step on many tensors of one dtype, one launch per
-    ``MUON_ADAMW_TENSORS_PER_LAUNCH`` tensors."""
+    ``MUON_ADAMW_TENSORS_PER_LAUNCH`` tensors.  Descriptors hold addresses only:
+    autograd is not told that P, m and v were written."""
     tensors = list(tensors)
     arr = (_lib.AdamwTensor * max(1, len(tensors)))()
     for i, t in enumerate(tensors):
@@ -606,7 +621,8 @@ def adamw8_step_grouped(tensors: Sequence[_lib.Adamw8Tensor], dtype: torch.dtype
     """One AdamW step with 8-bit states on many tensors of one dtype, in place
     on P and the states, one launch per ``MUON_ADAMW8_TENSORS_PER_LAUNCH``
     tensors.  ``step`` counts updates from 1.  The current device must be that
-    of the tensors."""
+    of the tensors.  Descriptors hold addresses only: autograd is not told that
+    P and the states were written."""
     arr, count = _c_array(_lib.Adamw8Tensor, tensors)
     st = _lib.lib().muon_adamw_byte_step_grouped(arr, count, dtype_code(dtype), float(betas[0]),
                                              float(betas[1]), float(eps), int(step),
@@ -621,6 +637,7 @@ def adamw8_step(P, G, state: AdamwState8, *, lr, step, seed: int = 0, betas=AUX_
     t = adamw8_tensor(P, G, state, lr=lr, weight_decay=weight_decay, seed=seed)
     with torch.cuda.device(P.device):
         adamw8_step_grouped([t], P.dtype, step=step, betas=betas, eps=eps, stream=stream)
+    _wrote(P, state.m_q, state.m_scale, state.r_q, state.r_scale)
 
 
 def adamw8_moments(states: Sequence[AdamwState8], dtype: torch.dtype = torch.float32, *, stream=None):
@@ -700,13 +717,16 @@ class AdamWStep:
         for i, (p, m, v, lr, wd) in enumerate(self.entries):
             if p.grad is None:
                 raise RuntimeError(f"AdamW parameter {i} has no gradient")
-            by_dtype.setdefault(p.dtype, []).append(
+            params, tensors = by_dtype.setdefault(p.dtype, ([], []))
+            params.append(p)
+            tensors.append(
                 adamw_tensor(p.data, p.grad, m, v, lr=lr, weight_decay=wd) if self.states is None else
                 adamw8_tensor(p.data, p.grad, self.states[i], lr=lr, weight_decay=wd,
                               seed=self._seed(i)))
         call = adamw_step_grouped if self.states is None else adamw8_step_grouped
-        for dtype, tensors in by_dtype.items():
+        for dtype, (params, tensors) in by_dtype.items():
             call(tensors, dtype, step=self.step_count, betas=self.betas, eps=self.eps)
+            _wrote(*params)
 
 
 class HybridMuonAdamW:

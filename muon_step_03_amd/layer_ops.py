@@ -22,7 +22,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from .api import _check, _ptr, dtype_code
+from .api import _check, _ptr, _wrote, dtype_code
 
 FORMATS = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
 _FORMAT_CODES = {torch.float8_e4m3fn: _lib.MUON_CKPT_E4M3, torch.int8: _lib.MUON_CKPT_INT8}
@@ -109,14 +109,6 @@ def _workspace(need, device, workspace):
         raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, "
                          f"{need} needed")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _wrote(*given):
-    """Tells autograd that tensors it did not make were written: a backward
-    pass that kept one of them then raises, as after PyTorch's own writes."""
-    for t in given:
-        if t is not None and not t.is_inference():
-            torch.autograd.graph.increment_version(t)
 
 
 class ActCheckpoint:

@@ -17,9 +17,8 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .api import _check, _ptr, dtype_code
-from .layer_ops import (ActCheckpoint, _away, _check_rows, _raw_stream, _ref,
-                        _there, _wrote)
+from .api import _check, _ptr, _wrote, dtype_code
+from .layer_ops import ActCheckpoint, _away, _check_rows, _raw_stream, _ref, _there
 
 
 class Weight8:
