@@ -565,12 +565,13 @@ static LinearPlan choose(LinearType type, bool across, int64_t count, int64_t to
 }
 
 LinearPlan linear_plan(LinearType type, bool across, int64_t count, int64_t tokens, int64_t k, int64_t n) {
-  const LinearPlan plan = choose(type, across, count, tokens, k, n);
-  // the largest grid, with whole turns of the 8 XCDs (rows that do not start on 16
-  // bytes may take tiles of 128 instead of 256, rows shorter than that take 64)
+  LinearPlan plan = choose(type, across, count, tokens, k, n);
+  // operands' rows of less than 16 bytes are loaded by the element, in tiles of 64
   const int64_t vec = type == LIN_BF16 ? 8 : 4;
-  const bool tiny = type <= LIN_F32 && (k < vec || (across && n < vec));
-  const int64_t side = plan == LIN_FEW ? 16 : plan == LIN_64 || tiny ? 64 : 128;
+  if (type <= LIN_F32 && plan != LIN_FEW && (k < vec || (across && n < vec))) plan = LIN_64;
+  // the largest grid, with whole turns of the 8 XCDs (rows that do not start on 16
+  // bytes may take tiles of 128 instead of 256)
+  const int64_t side = plan == LIN_FEW ? 16 : plan == LIN_64 ? 64 : 128;
   return (tokens / side + count + 2) * cdiv(n, side) >= (int64_t(1) << 24) - 8 ? LIN_NONE : plan;
 }
 

@@ -169,3 +169,17 @@ def test_grids_of_short_rows_count_their_smaller_tiles():
     assert k(0, 0, 1, tokens, 4096, 7, BF16) == -1
     assert k(1, 0, 1, tokens, 7, 4096, BF16) == -1
     assert k(0, 0, 1, tokens // 2, 4096, 7, BF16) >= 0
+
+
+@built
+@pytest.mark.parametrize("across,rows,cols,dtype", [
+    (0, 4096, 5, BF16), (0, 4096, 7, BF16), (0, 4096, 3, F32), (1, 5, 4096, BF16), (1, 4096, 7, BF16),
+    (1, 3, 4096, F32), (1, 4096, 2, F32)])
+def test_short_rows_are_reported_in_the_tiles_that_they_take(across, rows, cols, dtype):
+    """Rows of operands below 16 bytes always take tiles of 64 (or the kernel for
+    few tokens), those of outputs alone do not."""
+    k = _lib.lib().muon_linear_kernel
+    for tokens in (300, 5000, 16384, 200_000):
+        assert k(across, 0, 1, tokens, rows, cols, dtype) == _lib.MUON_LINEAR_TILES_64
+    assert k(0, 0, 1, 1, 40, 5, BF16) == _lib.MUON_LINEAR_FEW
+    assert k(0, 0, 1, 1 << 20, 5, 64, BF16) == _lib.MUON_LINEAR_TILES_128
