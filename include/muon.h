@@ -302,7 +302,7 @@ int muon_adamw_step_grouped(const muon_adamw_tensor* tensors, int64_t count, int
  *           of one call.
  *  Sizes    0 <= n <= MUON_ADAMW8_MAX_ELEMENTS; n == 0 skips the tensor.
  *  Scalars, stream, errors  as for muon_adamw_step_grouped; one launch per
- *           MUON_ADAMW8_TENSORS_PER_LAUNCH 56tensors.
+ *           MUON_ADAMW8_TENSORS_PER_LAUNCH tensors.
  */
 #define MUON_ADAMW8_MAX_ELEMENTS (((int64_t)1) << 35)
 #define MUON_ADAMW8_TENSORS_PER_LAUNCH 56
@@ -471,7 +471,12 @@ int muon_weight_grad(const void* dy, int64_t lddy, int dtype, const muon_ckpt* x
  * with count == 0 (its one offset is read like any other).  Products are exact
  * in float32 (bf16) or rounded to it (float32), accumulated in float32 and
  * rounded once to `dtype`.  Sizes, strides, stream and errors as for the other
- * layer operators; no workspace.
+ * layer operators; no workspace.  One launch computes a call: with n the width
+ * of the output and S the side of the tiles that muon_linear_kernel names (16
+ * for MUON_LINEAR_FEW, 64 for MUON_LINEAR_TILES_64, else 128),
+ *   (tokens / S + count + 2) * ceil(n / S) >= 2^24 - 8
+ * is refused with MUON_ERR_INVALID_SHAPE: some 2^36 outputs where S is 64, 2^30
+ * tokens of up to 64 outputs each; more tokens are several calls.
  */
 #define MUON_LINEAR_MAX_COUNT 1024
 int muon_linear_forward(const void* x, int64_t ldx, int dtype, const void* W,
@@ -523,7 +528,8 @@ typedef struct muon_weight8 {
   int64_t cols;
 } muon_weight8;
 
-/* Quantizes contiguous W [count][rows][cols] of `dtype`. */
+/* Quantizes contiguous W [count][rows][cols] of `dtype`; 2^24 blocks or more of
+ * MUON_WEIGHT_BLOCK x MUON_WEIGHT_BLOCK are refused with MUON_ERR_INVALID_SHAPE. */
 int muon_weight_quantize(const void* W, int dtype, const muon_weight8* out, void* stream);
 
 /* tokens and the inner size are those of the checkpoint; dtype: of y (dx). */

@@ -223,7 +223,9 @@ def linear_forward(x, W, *, offsets=None, dtype=None, out=None, stream=None) -> 
     GPU tensor of count + 1 running token totals, at most
     ``MUON_LINEAR_MAX_COUNT`` matrices; its values are not read on the host:
     those outside [0, tokens] or decreasing are bounded on the device.  Tokens of
-    no matrix give zeros."""
+    no matrix give zeros.  A call has at most 2^24 tiles of outputs
+    (``include/muon.h`` has the formula), which binds from some 2^36 outputs on,
+    or 2^30 tokens of a few outputs: larger ones raise, and are several calls."""
     if _away(x, stream):
         return _there(linear_forward, x, stream, W, offsets=offsets, dtype=dtype, out=out)
     return _product(x, W, offsets, dtype, out, across=False)

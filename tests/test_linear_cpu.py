@@ -183,3 +183,34 @@ def test_short_rows_are_reported_in_the_tiles_that_they_take(across, rows, cols,
         assert k(across, 0, 1, tokens, rows, cols, dtype) == _lib.MUON_LINEAR_TILES_64
     assert k(0, 0, 1, 1, 40, 5, BF16) == _lib.MUON_LINEAR_FEW
     assert k(0, 0, 1, 1 << 20, 5, 64, BF16) == _lib.MUON_LINEAR_TILES_128
+
+
+@built
+@pytest.mark.parametrize("across", [0, 1])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("count", [1, 37, 1024])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (7, 4096), (4096, 7), (64, 64), (65, 1), (1, 65), (513, 300), (BIG, 64), (64, BIG)])
+def test_the_largest_call_is_the_documented_one(across, dtype, count, rows, cols):
+    """Sizes are refused from (tokens / S + count + 2) * ceil(n / S) >= 2^24 - 8 on,
+    S the side of the tiles that muon_linear_kernel names."""
+    k = _lib.lib().muon_linear_kernel
+    n = cols if across else rows
+    for tokens in [1 << i for i in range(31)] + [3 << i for i in range(28)]:
+        which = k(across, 0, count, tokens, rows, cols, dtype)
+        sides = {_lib.MUON_LINEAR_FEW: 16, _lib.MUON_LINEAR_TILES_64: 64}
+        if which >= 0:
+            s = sides.get(which, 128)
+            assert (tokens // s + count + 2) * -(-n // s) < (1 << 24) - 8
+        else:       # (tiles of 128 are fewer than those of 64)
+            assert (tokens // 64 + count + 2) * -(-n // 64) >= (1 << 24) - 8
+    # what fits a GPU's memory in tiles of 64 without part tiles is taken
+    assert k(0, 0, 1, (1 << 24) - 1024, 4096, 1024, BF16) >= 0
+    assert k(across, 0, 1, (1 << 30) - (1 << 20), 1, 1, dtype) == _lib.MUON_LINEAR_TILES_64
+    assert k(across, 0, 1, 1 << 30, 1, 1, dtype) == -1
+
+
+@built
+def test_the_largest_weight():
+    """2^24 blocks of 128 x 128 are refused, with no overlap that could refuse them."""
+    w = weight(A[4], 0x7000000000000, 0x7f00000000000, 1024, 128 * 128, 128 * 128)
+    assert _lib.lib().muon_weight_quantize(0x10000000000, F32, w, None) == SHAPE
