@@ -207,6 +207,7 @@ def expert_linear(x, W, offsets, keep: Union[str, ActCheckpoint] = "e4m3", *,
     rows, cols] of the same type; the tokens [offsets[e], offsets[e + 1]) are
     expert e's (offsets: int64 GPU tensor of count + 1 running totals, read on
     the device only).  Tokens of no expert give zeros and get zero gradients.
+    A W that is not contiguous is copied in each call.
     keep, products: as for :func:`linear`."""
     if x.ndim != 2 or W.ndim != 3:
         raise ValueError(f"x must be [tokens, cols] and W [count, rows, cols], not {tuple(x.shape)} "
@@ -217,6 +218,7 @@ def expert_linear(x, W, offsets, keep: Union[str, ActCheckpoint] = "e4m3", *,
         raise ValueError(f"x has {x.shape[1]} columns, W {W.shape[2]}")
     if products is not None:
         return _linear8(x, W, offsets, keep, products)
+    W = W.contiguous()
     q = scale = None
     if torch.is_grad_enabled() and W.requires_grad:
         keep = _check_keep(keep, x, None)

@@ -253,3 +253,24 @@ def test_captured_training_pass(products):
         for a, b in zip(got, want):
             assert torch.equal(a, b), k
         del want
+
+
+@pytest.mark.parametrize("products", [None, "e4m3"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_weights_that_are_not_contiguous(products, dtype):
+    """Stacks kept with rows and columns exchanged, and slices of larger ones: the
+    bits of a contiguous copy, and gradients in the parameter's own layout."""
+    x, o = draw(50, 64, dtype=dtype, seed=1), off([3, 20, 20, 45])
+    dz = draw(50, 40, dtype=dtype, seed=2)
+    turned = leaf(draw(3, 64, 40, dtype=dtype, seed=3, scale=0.1))
+    wide = leaf(draw(3, 40, 96, dtype=dtype, seed=4, scale=0.1))
+    for p, view in ((turned, lambda t: t.transpose(1, 2)), (wide, lambda t: t[:, :, 16:80])):
+        X, Y, W = leaf(x), leaf(x), leaf(view(p.detach()).contiguous())
+        z, want = M.expert_linear(X, view(p), o, products=products), M.expert_linear(Y, W, o, products=products)
+        assert torch.equal(z, want)
+        z.backward(dz)
+        want.backward(dz)
+        assert torch.equal(X.grad, Y.grad) and torch.equal(view(p.grad), W.grad)
+        with torch.no_grad():
+            assert torch.equal(M.expert_linear(x, view(p), o, products=products), want)
+    assert not wide.grad[:, :, :16].any() and not wide.grad[:, :, 80:].any()
