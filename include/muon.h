@@ -233,7 +233,9 @@ int muon_step_grouped_noalloc(const muon_group* groups, int ngroups, int dtype,
  *           the bias corrections); lr and weight_decay finite (any sign).
  *  Sizes    0 <= n <= MUON_ADAMW_MAX_ELEMENTS; n == 0 skips the tensor.
  *  Stream, errors  as for the Muon entry points: validated before anything
- *           is enqueued, no allocation, no synchronisation.  The grouped call
+ *           is enqueued, no allocation, no synchronisation.  A count whose
+ *           tensors the host has no memory to list for the check of overlaps
+ *           is MUON_ERR_INVALID_ARGUMENT.  The grouped call
  *           updates all tensors in one launch per MUON_ADAMW_TENSORS_PER_LAUNCH
  *           tensors (very large tensors are split over several slots).
  */

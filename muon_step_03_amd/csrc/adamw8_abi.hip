@@ -2,6 +2,7 @@
 // the caller's stream.  Every argument is checked before the first HIP call.
 #include <algorithm>
 #include <cmath>
+#include <exception>
 #include <vector>
 
 #include "abi_util.h"
@@ -21,6 +22,17 @@ static_assert(MUON_ADAMW8_MAX_ELEMENTS / kAdam8Chunk <= kMaxBlocks, "a tensor fi
 // Ranges that may are inputs only (the states of a read).
 class Ranges {
  public:
+  // Room for those of `count` tensors, up to 6 each and 2 more: false where the host
+  // has none, for no C++ exception may leave a C entry point.
+  bool reserve(int64_t count) {
+    if (count > int64_t(1) << 40) return false;
+    try {
+      r_.reserve(size_t(count) * 6 + 2);
+      return true;
+    } catch (const std::exception&) {
+      return false;
+    }
+  }
   void add(const void* p, size_t bytes, bool out = true) {
     if (bytes) r_.push_back({reinterpret_cast<uintptr_t>(p), bytes, out});
   }
@@ -105,6 +117,7 @@ int muon_adamw_byte_step_grouped(const muon_adamw8_tensor* tensors, int64_t coun
     return MUON_ERR_INVALID_ARGUMENT;
   const size_t es = elem_size(dtype);
   Ranges r;
+  if (!r.reserve(count)) return MUON_ERR_INVALID_ARGUMENT;
   for (int64_t i = 0; i < count; ++i) {
     const muon_adamw8_tensor& x = tensors[i];
     if (!std::isfinite(x.lr) || !std::isfinite(x.weight_decay)) return MUON_ERR_INVALID_ARGUMENT;
@@ -152,6 +165,7 @@ int muon_adamw_byte_moments(const muon_adamw8_state* states, int64_t count, void
   if (count < 0 || (count > 0 && !states)) return MUON_ERR_INVALID_ARGUMENT;
   const size_t es = elem_size(dtype);
   Ranges ranges;
+  if (!ranges.reserve(count)) return MUON_ERR_INVALID_ARGUMENT;
   int64_t total = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (const int st = check_state(states[i]); st != MUON_OK) return st;

@@ -23,6 +23,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <dlfcn.h>
+#include <exception>
 #include <mutex>
 #include <vector>
 
@@ -639,7 +640,12 @@ int check_adamw_tensors(const muon_adamw_tensor* t, int64_t count, int dtype) {
     uintptr_t lo, hi;
   };
   std::vector<Range> r;
-  r.reserve(size_t(count) * 4);
+  if (count > int64_t(1) << 40) return MUON_ERR_INVALID_ARGUMENT;
+  try {      // no C++ exception may leave a C entry point
+    r.reserve(size_t(count) * 4);
+  } catch (const std::exception&) {
+    return MUON_ERR_INVALID_ARGUMENT;
+  }
   for (int64_t i = 0; i < count; ++i) {
     const muon_adamw_tensor& x = t[i];
     if (!std::isfinite(x.lr) || !std::isfinite(x.weight_decay)) return MUON_ERR_INVALID_ARGUMENT;

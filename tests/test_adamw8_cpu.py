@@ -180,3 +180,14 @@ def test_a_states_fields_are_not_assigned(field):
     their place would be neither read nor kept alive."""
     with pytest.raises(AttributeError):
         setattr(object.__new__(M.AdamwState8), field, torch.zeros(32))
+
+
+@built
+@pytest.mark.parametrize("count", [(1 << 40) + 1, 1 << 60, 1 << 62, (1 << 63) - 1])
+def test_counts_that_no_host_can_list(count):
+    """Refused before a tensor is looked at, with no C++ exception on the way."""
+    L, p = _lib.lib(), ctypes.c_void_p
+    one = (_lib.Adamw8Tensor * 1)()
+    assert L.muon_adamw_byte_step_grouped(one, count, 0, 0.8, 0.95, 1e-8, 1, None) == ARG
+    assert L.muon_adamw_byte_moments((_lib.Adamw8State * 1)(), count, p(A[6]), p(A[7]), 0, None) == ARG
+    assert L.muon_adamw_step_grouped((_lib.AdamwTensor * 1)(), count, 0, 0.8, 0.95, 1e-8, 1, None) == ARG
