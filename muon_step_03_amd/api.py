@@ -352,7 +352,7 @@ class MuonStep:
     Parameters are grouped by (shape, dtype); each group keeps device pointer
     tables and fp32 momentum buffers, and :meth:`step` updates every group in
     one launch sequence per dtype from the parameters' ``.grad``, on the
-    current stream.
+    current stream of their device (one for all of a dtype).
 
     ``stats_order`` lists the parameter indices in the order of the rows of
     the optional ``stats`` buffer of :meth:`step` (``MUON_STATS_PER_MATRIX``
@@ -445,7 +445,8 @@ class MuonStep:
             n = sum(len(idx) for idx in shapes.values())
             st = None if stats is None else \
                 stats[offset * _lib.MUON_STATS_PER_MATRIX:(offset + n) * _lib.MUON_STATS_PER_MATRIX]
-            muon_step_grouped(groups, dtype, workspace=ws, stats=st, device=ws.device, **self.hp)
+            with torch.cuda.device(ws.device):
+                muon_step_grouped(groups, dtype, workspace=ws, stats=st, device=ws.device, **self.hp)
             _wrote(*(self.params[i] for idx in shapes.values() for i in idx))
             offset += n
 
@@ -671,8 +672,8 @@ def adamw8_moments(states: Sequence[AdamwState8], dtype: torch.dtype = torch.flo
 
 class AdamWStep:
     """AdamW over parameter groups (dicts with ``params``, ``lr`` and optional
-    ``weight_decay``), every parameter of one dtype updated by one grouped call
-    per step from its ``.grad``.
+    ``weight_decay``), every parameter of one dtype (and device) updated by one
+    grouped call per step from its ``.grad``, on that device's current stream.
 
     ``states``: "f32" keeps both moments in float32, "8bit" in an
     :class:`AdamwState8` per parameter (``self.states``), whose roundings
@@ -713,19 +714,20 @@ class AdamWStep:
     @torch.no_grad()
     def step(self):
         self.step_count += 1
-        by_dtype = {}
+        calls = {}
         for i, (p, m, v, lr, wd) in enumerate(self.entries):
             if p.grad is None:
                 raise RuntimeError(f"AdamW parameter {i} has no gradient")
-            params, tensors = by_dtype.setdefault(p.dtype, ([], []))
+            params, tensors = calls.setdefault((p.device, p.dtype), ([], []))
             params.append(p)
             tensors.append(
                 adamw_tensor(p.data, p.grad, m, v, lr=lr, weight_decay=wd) if self.states is None else
                 adamw8_tensor(p.data, p.grad, self.states[i], lr=lr, weight_decay=wd,
                               seed=self._seed(i)))
         call = adamw_step_grouped if self.states is None else adamw8_step_grouped
-        for dtype, (params, tensors) in by_dtype.items():
-            call(tensors, dtype, step=self.step_count, betas=self.betas, eps=self.eps)
+        for (device, dtype), (params, tensors) in calls.items():
+            with torch.cuda.device(device):
+                call(tensors, dtype, step=self.step_count, betas=self.betas, eps=self.eps)
             _wrote(*params)
 
 
