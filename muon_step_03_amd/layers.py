@@ -186,7 +186,8 @@ def linear(x, W, keep: Union[str, ActCheckpoint] = "e4m3", *,
     checkpoint of x with W in 8 bits (scales for 32 columns and for 128 x 128
     elements), and in the backward pass dy, in 8 bits too, with the same W; a
     :class:`Weight8` of W, made once after each optimizer step, spares the
-    micro-batches the quantizing."""
+    micro-batches the quantizing.  With bfloat16 x the sums hold fewer bits than
+    float32 (see :func:`linear_forward`), with float32 x they do not."""
     if W.ndim != 2:
         raise ValueError(f"W must be 2-D, it has {W.ndim} dims")
     if x.dtype != W.dtype:
