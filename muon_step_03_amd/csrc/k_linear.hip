@@ -108,7 +108,7 @@ constexpr int elem_bytes() { return TYPE == LIN_BF16 ? 2 : TYPE == LIN_F32 ? 4 :
 // than a chunk by elements.
 enum LinearPath { DIRECTLY, BY_VECTORS, BY_ELEMENTS };
 template <LinearType TYPE, bool ACROSS, LinearPath PATH, class S>
-__global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(const Linear p, int tiles_n) {
+__global__ __launch_bounds__(S::THREADS, 2) void linear_kernel(const Linear p, int tiles_n) {
   constexpr int ES = elem_bytes<TYPE>(), BK = ROWB / ES;
   constexpr int BM = S::BM, BN = S::BN, MT = S::MT, NT = S::NT, THREADS = S::THREADS;
   constexpr bool E4M3 = TYPE >= LIN_E4M3, DIRECT = PATH == DIRECTLY, TINY = PATH == BY_ELEMENTS;
@@ -117,9 +117,10 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
   constexpr int XS_BYTES = E4M3 ? S::NW * 256 : 0;        // x scales of a step
   constexpr int STAGE = X_BYTES + W_BYTES + XS_BYTES;
   constexpr int STAGES = DIRECT ? S::STAGES : 2;
-  constexpr int WS_AT = STAGES * STAGE, WS_BYTES = E4M3 ? (BN + SIDE - 1) / SIDE * (MUON_MAX_DIM / SIDE) : 0;
+  static_assert(SIDE % BN == 0, "a tile's outputs share the scales of a weight");
+  constexpr int WS_AT = STAGES * STAGE, WS_BYTES = E4M3 ? MUON_MAX_DIM / SIDE : 0;
   constexpr int LDS_BYTES = WS_AT + WS_BYTES;
-  static_assert(LDS_BYTES <= (S::NW == 8 ? 160 : 80) * 1024, "LDS");
+  static_assert(LDS_BYTES <= 80 * 1024, "LDS");
   static_assert(S::NW * window_bytes<NT>() <= LDS_BYTES, "the epilogue's windows");
   __shared__ __attribute__((aligned(1024))) char smem_raw[LDS_BYTES];
   LDS_AS char* smem = (LDS_AS char*)smem_raw;
@@ -342,8 +343,7 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
 #pragma unroll
       for (int a = 0; a < MT; ++a)
         sx[a] = *reinterpret_cast<const LDS_AS uint32_t*>(s + X_BYTES + W_BYTES + (xr0 + a * 32 + (lane & 31)) * 4);
-      const uint32_t wsc = *reinterpret_cast<const LDS_AS uint8_t*>(smem + WS_AT + wr0 / SIDE * (MUON_MAX_DIM / SIDE) + k);
-      static_assert(SIDE % (NT * 32) == 0, "a wave's outputs share a scale");
+      const uint32_t wsc = *reinterpret_cast<const LDS_AS uint8_t*>(smem + WS_AT + k);
       if constexpr (TYPE == LIN_E4M3_EXACT) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -429,12 +429,8 @@ __global__ __launch_bounds__(S::THREADS, S::NW == 8 ? 1 : 2) void linear_kernel(
   if (steps > 0) {
     if constexpr (E4M3) {      // the weight's scales, all of k
       const uint8_t* ws = p.w_scale + at.e * p.ws_stride + int64_t(n0 / SIDE) * p.ws_row;
-#pragma unroll
-      for (int b = 0; b < (BN + SIDE - 1) / SIDE; ++b)
-        if (n0 + b * SIDE < p.n)
-          for (int k = t; k < steps; k += THREADS)
-            *reinterpret_cast<LDS_AS uint8_t*>(smem + WS_AT + b * (MUON_MAX_DIM / SIDE) + k) =
-                ws[b * p.ws_row + k * p.ws_col];
+      for (int k = t; k < steps; k += THREADS)
+        *reinterpret_cast<LDS_AS uint8_t*>(smem + WS_AT + k) = ws[k * p.ws_col];
     }
     if constexpr (DIRECT) {
       std::true_type end;
