@@ -652,9 +652,9 @@ def adamw8_moments(states: Sequence[AdamwState8], dtype: torch.dtype = torch.flo
     for i, s in enumerate(states):
         if type(s) is not AdamwState8:
             raise TypeError(f"states[{i}] must be an AdamwState8")
-        if s.device != device:
-            raise ValueError(f"states[{i}] is on {s.device}, expected {device}")
-        total += s.n
+        if s._device != device:
+            raise ValueError(f"states[{i}] is on {s._device}, expected {device}")
+        total += s._n
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the states on {device}")
     code = dtype_code(dtype)
