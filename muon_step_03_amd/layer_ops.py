@@ -163,7 +163,7 @@ class ActCheckpoint:
         self._q = self._buffer[:size].view(self._store).view(tokens, _lib.ckpt_q_pitch(cols))
         self._scale = self._buffer[size:].view(tokens, _lib.ckpt_scale_pitch(cols))
 
-    def __reduce__(self):      # copies and pickles have tensors of their own
+    def __reduce__(self):      # deep copies and pickles have tensors of their own
         return ActCheckpoint, (self.q, self.scale, self.cols)
 
     def _written(self):

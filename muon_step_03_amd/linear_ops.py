@@ -29,7 +29,7 @@ class Weight8:
     column blocks] of 128 x 128 elements.  An element stands for
     ``q * 2^(scale - 127)``."""
 
-    __slots__ = ("_q", "_q_t", "_scale", "_buffer", "shape", "device", "_c")
+    __slots__ = ("_q", "_q_t", "_scale", "_buffer", "_shape", "_device", "_c")
 
     def __init__(self, q: torch.Tensor, q_t: torch.Tensor, scale: torch.Tensor):
         for name, t, dtype in (("q", q, torch.float8_e4m3fn), ("q_t", q_t, torch.float8_e4m3fn),
@@ -52,7 +52,7 @@ class Weight8:
             if t.device != device:
                 raise ValueError(f"{name} is on {t.device}, q on {device}")
         self._q, self._q_t, self._scale, self._buffer = q, q_t, scale, None
-        self.shape, self.device = (*lead, rows, cols), device
+        self._shape, self._device = (*lead, rows, cols), device
         self._c = _lib.Weight8(q.data_ptr(), q_t.data_ptr(), scale.data_ptr(),
                                lead[0] if lead else 1, rows, cols)
 
@@ -73,13 +73,13 @@ class Weight8:
         if not w._buffer.is_cuda:
             raise ValueError(f"a Weight8 must be on a GPU, not on {w._buffer.device}")
         w._q = w._q_t = w._scale = None
-        w.shape, w.device = (*lead, rows, cols), w._buffer.device
+        w._shape, w._device = (*lead, rows, cols), w._buffer.device
         at = w._buffer.data_ptr()
         w._c = _lib.Weight8(at, at + a, at + a + b, n, rows, cols)
         return w
 
     def _split(self):
-        *lead, rows, cols = self.shape
+        *lead, rows, cols = self._shape
         pr, pc = (rows + 127) // 128, (cols + 127) // 128
         n = lead[0] if lead else 1
         a, b = n * rows * pc * 128, n * cols * pr * 128
@@ -106,7 +106,15 @@ class Weight8:
             self._split()
         return self._scale
 
-    def __reduce__(self):      # copies and pickles have tensors of their own
+    @property
+    def shape(self):
+        return self._shape
+
+    @property
+    def device(self) -> torch.device:
+        return self._device
+
+    def __reduce__(self):      # deep copies and pickles have tensors of their own
         return Weight8, (self.q, self.q_t, self.scale)
 
     @property

@@ -214,3 +214,10 @@ def test_the_largest_weight():
     """2^24 blocks of 128 x 128 are refused, with no overlap that could refuse them."""
     w = weight(A[4], 0x7000000000000, 0x7f00000000000, 1024, 128 * 128, 128 * 128)
     assert _lib.lib().muon_weight_quantize(0x10000000000, F32, w, None) == SHAPE
+
+
+@pytest.mark.parametrize("field", ["q", "q_t", "scale", "shape", "device"])
+def test_a_weights_fields_are_not_assigned(field):
+    """The library reads the tensors, and the sizes, that a weight was made of."""
+    with pytest.raises(AttributeError):
+        setattr(object.__new__(M.Weight8), field, None)
