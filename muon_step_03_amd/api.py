@@ -110,9 +110,7 @@ def check_stats(stats, n_matrices: int, device=None) -> None:
 def _wrote(*given):
     """Tells autograd that tensors it did not make were written: a backward
     pass that kept one of them then raises, as after PyTorch's own writes."""
-    for t in given:
-        if t is not None and not t.is_inference():
-            torch.autograd.graph.increment_version(t)
+    torch.autograd.graph.increment_version([t for t in given if t is not None])
 
 
 def _ptr(t) -> int:
@@ -721,8 +719,8 @@ class AdamWStep:
             params, tensors = calls.setdefault((p.device, p.dtype), ([], []))
             params.append(p)
             tensors.append(
-                adamw_tensor(p.data, p.grad, m, v, lr=lr, weight_decay=wd) if self.states is None else
-                adamw8_tensor(p.data, p.grad, self.states[i], lr=lr, weight_decay=wd,
+                adamw_tensor(p, p.grad, m, v, lr=lr, weight_decay=wd) if self.states is None else
+                adamw8_tensor(p, p.grad, self.states[i], lr=lr, weight_decay=wd,
                               seed=self._seed(i)))
         call = adamw_step_grouped if self.states is None else adamw8_step_grouped
         for (device, dtype), (params, tensors) in calls.items():
