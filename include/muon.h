@@ -289,6 +289,9 @@ int muon_adamw_step_grouped(const muon_adamw_tensor* tensors, int64_t count, int
  *   x = (i mod 2^32) 0x9e3779b1 + (i / 2^32) 0x85ebca77 + seed   (mod 2^32)
  *   x = (x ^ x >> 16) 0x7feb352d;  x = (x ^ x >> 15) 0x846ca68b;  x = x ^ x >> 16
  *
+ * (the second line is the one-to-one mixing of 32 bits that C. Wellons published
+ * in "Prospecting for Hash Functions", 2018; the first one's factors are odd).
+ *
  * Rounding to nearest would hold a slowly moving average where it is: with
  * beta2 = 0.999 no step of r reaches half a step of the format.  The caller
  * gives every tensor and step another seed; the same seed gives the same

@@ -110,7 +110,9 @@ def check_stats(stats, n_matrices: int, device=None) -> None:
 def _wrote(*given):
     """Tells autograd that tensors it did not make were written: a backward
     pass that kept one of them then raises, as after PyTorch's own writes."""
-    torch.autograd.graph.increment_version([t for t in given if t is not None])
+    given = [t for t in given if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
 
 
 def _ptr(t) -> int:
@@ -703,7 +705,8 @@ class AdamWStep:
 
     def _seed(self, i):
         """Of parameter i in the current step: any two differ, by no fixed step (the
-        elements' numbers enter their random bits by a fixed one)."""
+        elements' numbers enter their random bits by a fixed one).  The mixing is the
+        one-to-one hash of 32 bits that T. Mueller published on Stack Overflow."""
         n = self.step_count * len(self.entries) + i & 0xffffffff
         n = (n ^ n >> 16) * 0x45d9f3b & 0xffffffff
         n = (n ^ n >> 16) * 0x45d9f3b & 0xffffffff

@@ -14,11 +14,14 @@
 //
 // Tiles of 64 x 64 (four steps on their way to LDS) while those of 128 x 128 (two
 // blocks per CU, a step ahead) would not fill the chip: bound by latency there,
-// then by the loads from the L2.  Measured on one MI355X: bf16 input gradient of
-// 49152 tokens, 64 x 1408 x 512, uneven, 128 x 128: 89 us (790 TFLOP/s); 1023 tokens
-// of 7 x 777 x 1001, no row on 16 bytes, 64 x 64: 16.5 us; 1024 tokens of 1024 x 1024
-// 10.3 us.  float32: 16384 tokens of 1024 x 1024 261 us, 131 TFLOP/s of the 143 that
-// a large library product reaches; 2049 tokens of 7 x 1001 x 777 51 us.
+// then by the loads from the L2.  Measured on one MI355X, calls between others: bf16
+// input gradient of 49152 tokens, 64 x 1408 x 512, uneven, 128 x 128: 110 us (650
+// TFLOP/s), over the same operands again and again, which the caches hold then, 83 to
+// 92; 1023 tokens of 7 x 777 x 1001, no row on 16 bytes, 64 x 64: 15.9 us; 1024 tokens
+// of 1024 x 1024 10.3 us.  float32: 16384 tokens of 1024 x 1024 248 us forward, 245
+// back, 140 TFLOP/s as the library's product; 2049 tokens of 7 x 1001 x 777 46 us
+// forward, 47 back; 16384 of 64 x 1408 x 512 233 and 257 (102 and 92 TFLOP/s).  8 bits
+// to float32, 16384 tokens of 4096 x 1024: 142 us forward, 119 back (970 and 1155).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -35,7 +38,7 @@ namespace {
 // of a row.  Lane l, register 4 g + i of a 32 x 32 block holds token l % 32,
 // output 8 g + 4 (l / 32) + i.  STREAM: the L2 need not keep them, as for calls that
 // fill the chip with the larger tiles (49152 tokens of 64 x 1408 x 512, input
-// gradient: 110 -> 94 us).
+// gradient, over the same operands again: 110 -> 94 us).
 template <int NT>
 constexpr int window_bytes() { return 32 * (32 * NT + 4) * 4; }
 template <int MT, int NT, bool STREAM>
@@ -547,9 +550,12 @@ static LinearPlan choose(LinearType type, bool across, int64_t count, int64_t to
   if (n64 <= 640) return LIN_64;
   if (type == LIN_E4M3_EXACT) return LIN_128;
   // Blocks that stay, from two per CU on (16384 tokens of 64 x 1408 x 512: 40 against
-  // 47; across the rows they gain nothing), and their tiles of 256 x 256, which read
-  // half as much, where whole rounds of them do not lose it again (16384 tokens of
-  // 4096 x 2048: 227, of 128 x 128 255; of 1408 x 512: 36 against 30).
+  // 47), and not across the rows, where they gained nothing before they stored whole
+  // lines (tried since, between other calls: 16384 tokens of 64 x 1408 x 512 53 us
+  // against 56 in the tiles here, 49152 109 against 111, of 64 x 512 x 1408 110 against
+  // 128, 32768 of 16 x 2048 x 1024 165 against 179: not built); and their tiles of
+  // 256 x 256, which read half as much, where whole rounds of them do not lose it again
+  // (16384 tokens of 4096 x 2048: 227, of 128 x 128 255; of 1408 x 512: 36 against 30).
   const double steps = double(k) * (type == LIN_E4M3 ? 1 : 2) / ROWB;
   const double step256 = type == LIN_E4M3 ? 1.22 : across ? 1.62 : 1.34, step128 = across ? 0.88 : 0.93;
   const double us256 = std::ceil(n256 / 256) * (step256 * steps + 10),
