@@ -75,7 +75,7 @@ def _check_rows(name, t, device=None, shape=None, dtype=None, contiguous=False):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if rows and cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     ld = cols if rows <= 1 else t.stride(0)
     if ld < cols or (contiguous and ld != cols):

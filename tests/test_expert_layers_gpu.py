@@ -274,3 +274,20 @@ def test_weights_that_are_not_contiguous(products, dtype):
         with torch.no_grad():
             assert torch.equal(M.expert_linear(x, view(p), o, products=products), want)
     assert not wide.grad[:, :, :16].any() and not wide.grad[:, :, 80:].any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_no_tokens_and_an_expanded_gradient(dtype):
+    """A batch without tokens whose outputs are summed: the gradient that autograd
+    hands over is an expanded one of no elements, of any strides."""
+    gain, w, W = leaf(draw(64, dtype=dtype)), leaf(draw(40, 64, dtype=dtype)), leaf(draw(2, 40, 64, dtype=dtype))
+    o = off([0, 0, 0])
+    for layer, p in ((lambda x: M.layer_norm(x, gain), gain), (lambda x: M.layer_norm(x, gain, keep="e4m3"), gain),
+                     (lambda x: M.linear(x, w), w), (lambda x: M.linear(x, w, products="e4m3"), w),
+                     (lambda x: M.expert_linear(x, W, o), W), (lambda x: M.expert_linear(x, W, o, products="e4m3"), W)):
+        for shape in ((0, 64), (2, 0, 64)) if p is not W else ((0, 64),):
+            x, p.grad = torch.zeros(shape, dtype=dtype, device=DEV, requires_grad=True), None
+            layer(x).sum().backward()
+            assert x.grad.shape == x.shape and p.grad.shape == p.shape and not p.grad.any()
+    x = torch.zeros(1, 1, dtype=dtype, device=DEV).expand(0, 64)
+    assert M.linear_forward(x, w.detach()).shape == (0, 40)
