@@ -677,7 +677,8 @@ class AdamWStep:
 
     ``states``: "f32" keeps both moments in float32, "8bit" in an
     :class:`AdamwState8` per parameter (``self.states``), whose roundings
-    follow from ``seed``, the step and the parameter's place."""
+    follow from ``seed``, the step and the parameter's place.  A step captured
+    into a graph replays the step count and the seeds of its capture."""
 
     def __init__(self, param_groups, betas=AUX_BETAS, eps=AUX_EPS,
                  weight_decay=AUX_WEIGHT_DECAY, states="f32", seed: int = 0):
