@@ -125,3 +125,22 @@ def test_what_a_group_keeps(shape):
             y = M.linear_forward(ck, w8, dtype=BF16)
             assert bool((y == (float(int(small / 8) * 8) if near else small)).all()), (at, small)
             assert bool((M.linear_forward(ck, w8, dtype=F32) == small).all()), (at, small)
+
+
+@pytest.mark.parametrize("tokens,rows", [(5, 300), (700, 500)])
+@pytest.mark.parametrize("least,kept", [(-9, 2), (-8, 3), (-7, 4), (-6, 5), (-5, 5)])
+def test_what_a_group_of_subnormals_keeps(tokens, rows, least, kept):
+    """2^least times 2^8, minus that, and 2^least times 2^-j: with E = max(least, -6)
+    + 8 the last one is kept from 2^(E - 13) on, so up to j = kept."""
+    f8, k = torch.float8_e4m3fn, 256
+    x, W = torch.zeros(tokens, k, device=DEV), torch.zeros(rows, k, device=DEV)
+    x[:, 0], x[:, 1], x[:, 2] = 2.0 ** least, -2.0 ** least, 2.0 ** least
+    W[:, :2] = 256.0
+    W[:, 3] = 448.0      # each block's scale is 1
+    ck = M.ActCheckpoint(x.to(f8), torch.full((tokens, 8), 127, dtype=torch.uint8, device=DEV), k)
+    for j in range(-8, 7):
+        W[:, 2] = 2.0 ** -j
+        w8 = M.weight_quantize(W)
+        assert bool((w8.scale[:, 0] == 127).all())
+        y = M.linear_forward(ck, w8, dtype=BF16)
+        assert bool((y == (2.0 ** (least - j) if j <= kept else 0.0)).all()), j
